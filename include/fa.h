@@ -234,6 +234,153 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* v8, float q_sca
                      const uint8_t* block_mask, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------- paged cache
+ * Serving over a key/value cache kept in pages: fa_cache_plan hands out pages and
+ * builds the slot map of a step's new rows, fa_rope_append rotates q and k and
+ * writes k and v to their slots, fa_tree_fwd attends over the pages, and
+ * fa_cache_commit moves the rows of an accepted draft to the front. The batch is
+ * ragged and packed: request b owns rows cu[b] .. cu[b+1]-1 of the [rows][heads][d]
+ * tensors. All lengths, tables and maps live on the device, so a step can be
+ * captured in a CUDA graph and replayed with other lengths.
+ */
+
+/*
+ * A paged cache. Row r of page p, head h starts at element
+ * p*page_stride + h*head_stride + r*row_stride of k and of v (so pages laid out
+ * [head][row][d] or [row][head][d], and one layer of a larger pool, are all
+ * reachable). k, v: DEVICE, 16-byte aligned; the strides are positive multiples
+ * of 8 elements; page_size is a power of two, 8..1024; d as for the forward
+ * entry points; num_pages * page_size <= 2^31 - 1.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  fa_dtype dtype;
+  int num_pages, page_size, H_kv, d;
+  long long page_stride, head_stride, row_stride;
+} fa_kv_cache;
+
+/*
+ * Packed rows [rows][heads][d]: head h of row t starts at element
+ * t*row_stride + h*head_stride; its d elements are contiguous. DEVICE, 16-byte
+ * aligned, strides multiples of 8 elements (a slice of a fused projection is
+ * fine).
+ */
+typedef struct {
+  void* data;
+  long long row_stride, head_stride;
+} fa_rows;
+
+/*
+ * Pages, slot map, positions and tree masks of a step, from the requests'
+ * lengths. Request b holds ctx_len[b] cached rows and adds n_b = cu_new[b+1] -
+ * cu_new[b] new ones; it then needs ceil((ctx_len[b] + n_b) / page_size) pages.
+ *   1. Requests that hold more give the rest back: their last pages are pushed on
+ *      the free list, in the order of the requests, and the table entries set to -1
+ *      (a request with no rows at all gives back everything).
+ *   2. Requests that need more take them from the end of the free list, in the order
+ *      of the requests. Request b is granted iff it needs none, or the needs of
+ *      requests 0..b together do not exceed the free pages. A request whose
+ *      ctx_len is negative, whose n_b is negative or over max_new, or which needs
+ *      more than max_pages pages, takes no part and is refused.
+ *   3. Granted: n_pages[b] and block_table row b are updated and seq_len[b] =
+ *      ctx_len[b] + n_b. Refused: pages and table stay, seq_len[b] = 0.
+ *   4. slot[cu_new[b] + i] = row ctx_len[b] + i as page * page_size + row in page, -1
+ *      if b was refused; position[cu_new[b] + i] = ctx_len[b] + i, or with `parent`
+ *      ctx_len[b] + the token's depth in its tree. Rows of no request (from
+ *      cu_new[B] to `rows`) get slot -1 and position 0.
+ *   5. With `parent` (request-local index of each new token's parent, -1 for a child
+ *      of the cached context; an entry outside [-1, i) counts as -1), tree_mask
+ *      [rows][ceil(max_new/64)] gets each token's branch: bit j of the row (word
+ *      j / 64, bit j % 64) is set iff new token j of the request is the token
+ *      itself or one of its ancestors. Rows of no request keep theirs.
+ * block_table int32 [B][max_pages]; n_pages int32 [B] (pages held); free_list int32
+ * [num_pages], of which the first *free_count are free; ctx_len, seq_len [B]; cu_new
+ * [B+1]; slot, position, parent [rows], all int32 on the DEVICE. block_table,
+ * n_pages, free_list and free_count are the cache's state and updated in place:
+ * calls on one cache must be ordered. parent and tree_mask are both given or both
+ * NULL. 1 <= B <= 4096, 0 <= rows, 1 <= max_new (with parent: <= 512, else
+ * FA_ERR_UNSUPPORTED). One launch.
+ */
+#define FA_TREE_MAX 512
+fa_status fa_cache_plan(int B, int rows, int max_new, int page_size, int num_pages, int max_pages,
+                        const int32_t* ctx_len, const int32_t* cu_new, const int32_t* parent, int32_t* block_table,
+                        int32_t* n_pages, int32_t* free_list, int32_t* free_count, int32_t* seq_len, int32_t* slot,
+                        int32_t* position, uint64_t* tree_mask, cudaStream_t stream);
+
+/*
+ * Rotary positions over several axes. Of each row x the first rot elements are
+ * rotated in pairs and the rest copied: pair i of token (b, n) turns by the angle
+ *   positions[axis[i]][b][n] * inv_freq[i]
+ * (the caller's tables choose the frequencies and which pairs belong to time,
+ * height or width; one axis is ordinary rotary), (x, y) -> (x cos - y sin,
+ * x sin + y cos). Pair i is elements (i, i + rot/2), or (2i, 2i+1) with pairs != 0.
+ * inverse != 0 turns back: the rotation is orthogonal, so this is also its
+ * gradient. Angles are reduced in 64 bits, so far positions lose nothing.
+ * x, out [B, H, N, d] with element strides of b, h and n (multiples of 8; the d
+ * elements contiguous; 16-byte aligned); out may be x itself, but must not overlap
+ * it in another way. positions int32 [n_axes][B][N] with element strides of axis and
+ * b (0: shared by the batch); inv_freq fp32 [rot/2]; axis uint8 [rot/2], an entry
+ * >= n_axes leaves its pair unturned. rot a multiple of 16, 16..d; 1 <= n_axes <= 8;
+ * d as for the forward entry points.
+ */
+fa_status fa_rope(fa_dtype dtype, const void* x, void* out, int B, int H, int N, int d, const long long x_strides[3],
+                  const long long out_strides[3], const int32_t* positions, long long pos_axis_stride,
+                  long long pos_b_stride, int n_axes, const float* inv_freq, const uint8_t* axis, int rot, int inverse,
+                  int pairs, cudaStream_t stream);
+
+/*
+ * The same rotation of a step's new q and k, with k and v written to the cache:
+ * q -> q_out [rows][Hq][d], k and v [rows][H_kv][d] -> row slot[t] of the cache (page
+ * slot / page_size, row slot % page_size). A slot outside the cache (-1) writes
+ * nothing; two rows with one slot leave either. positions int32 [n_axes][rows] with
+ * an axis stride. q and q_out may both be NULL (k and v only) and q_out may be q.
+ * rot = 0 rotates nothing (positions, inv_freq, axis are not read). One launch.
+ */
+fa_status fa_rope_append(const fa_kv_cache* cache, int rows, int Hq, const fa_rows* q, const fa_rows* k,
+                         const fa_rows* v, const fa_rows* q_out, const int32_t* slot, const int32_t* positions,
+                         long long pos_axis_stride, int n_axes, const float* inv_freq, const uint8_t* axis, int rot,
+                         int pairs, cudaStream_t stream);
+
+/*
+ * Attention of a step's new rows over the paged cache, exact as fa_fwd_qk is.
+ * Request b's rows are q rows cu_q[b] .. cu_q[b+1]-1 (n_b of them, at most max_q) and
+ * its keys the first seq_len[b] rows of its pages; the last n_b keys are its own new
+ * tokens, already written. Head h reads cache head h / (Hq / H_kv). Row i sees key j
+ * iff j < seq_len[b] and
+ *   tree_mask NULL:  j <= i + seq_len[b] - n_b     (a chain: decoding, prompt chunks)
+ *   otherwise:       j < seq_len[b] - n_b, or bit j - (seq_len[b] - n_b) of the row's
+ *                    tree_mask [rows][ceil(max_q/64)] is set (a drafted tree).
+ * Keys on a page index outside [0, num_pages) are not seen. A row that sees no key
+ * gets O = 0, lse = -inf. o [rows][Hq][d]; lse fp32 [rows][Hq], natural log as
+ * fa_fwd. Rows of no request stay as they were. What the cache holds behind
+ * seq_len[b] is never used, whatever it is; K and V of a request's own keys that some
+ * row does not see must be finite in V (P = 0 there multiplies them).
+ * block_table int32 [B][max_pages], 16-byte aligned q, o. Hq a multiple of H_kv;
+ * 1 <= B <= 4096; max_q >= 1, with tree_mask <= FA_TREE_MAX. workspace: DEVICE,
+ * 256-byte aligned, fa_tree_fwd_workspace_size() bytes, contents irrelevant; calls
+ * that may overlap need one each. scale finite.
+ */
+size_t fa_tree_fwd_workspace_size(int B, int rows, int max_q, int Hq, int H_kv, int d);
+fa_status fa_tree_fwd(const fa_kv_cache* cache, const fa_rows* q, const fa_rows* o, float* lse, int B, int rows,
+                      int max_q, int Hq, int max_pages, const int32_t* block_table, const int32_t* cu_q,
+                      const int32_t* seq_len, const uint64_t* tree_mask, float softmax_scale, void* workspace,
+                      cudaStream_t stream);
+
+/*
+ * Keeps the accepted path of each request's draft: row ctx_len[b] + accepted[b][j] of
+ * the cache moves to row ctx_len[b] + j, for j < n_accepted[b], and new_len[b] =
+ * ctx_len[b] + the rows kept. accepted int32 [B][max_accept] holds request-local
+ * indices of new tokens, strictly increasing (a path from the root is); the path ends
+ * before the first entry that is not larger than the one before (or is negative), or
+ * whose row has no page in the table. new_len may be ctx_len. DEVICE pointers; ctx_len,
+ * n_accepted, new_len int32 [B]. One launch.
+ */
+fa_status fa_cache_commit(const fa_kv_cache* cache, int B, int max_pages, int max_accept, const int32_t* block_table,
+                          const int32_t* ctx_len, const int32_t* accepted, const int32_t* n_accepted,
+                          int32_t* new_len, cudaStream_t stream);
+
+/*
  * Debug: the dropout draws u (uint8) of every (head, query row, key) for
  * B*H heads, Nq query rows, Nk keys, written to two DEVICE buffers of
  * B*H*Nq*Nk bytes, [bh][i][j]: row_major through the generator path of the

@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
-SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_splitkv.cu", "fa_decode.cu", "fa_dropout.cu", "fa_bwd_noalloc.cu"]
+SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_splitkv.cu", "fa_decode.cu", "fa_dropout.cu", "fa_bwd_noalloc.cu",
+           "fa_cache_api.cu", "fa_cache.cu", "fa_rope.cu", "fa_tree.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]
