@@ -1,95 +1,144 @@
-// Attention of a ragged batch's new rows over the paged cache (fa_tree_fwd).
-//
-// One CTA per row and head, a warp per key in turn, each warp with its own running
-// maximum, sum and O (the online-softmax recurrence), merged at the end.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
-#include <cmath>
-#include <cstdint>
+// Host launcher of the paged tree attention.
+#include "fa_tree.cuh"
 
 #include "fa_cache.h"
+#include "tma_host.h"
 
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
+// Columns of the MMA: the smallest tile that holds a request's rows of one cache head.
+int row_tile(int max_q, int group) {
+  const long long rows = static_cast<long long>(max_q) * group;
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+}
 
-template <bool BF16>
-__device__ __forceinline__ float widen(uint16_t x) {
-  if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(x) << 16);
-  else return __half2float(*reinterpret_cast<const __half*>(&x));
+int padded_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
+
+// Units that are many and long are not cut: a CTA each.
+bool by_unit(int rows, int max_q, int Hq, int H_kv, int tile) {
+  const long long units = static_cast<long long>(H_kv) * ((static_cast<long long>(rows) * (Hq / H_kv) + tile - 1) / tile);
+  return static_cast<long long>(max_q) * (Hq / H_kv) >= 512 && units >= 4 * tree::kMaxWorkers;
+}
+
+struct Workspace {
+  size_t part_lse, cuts, total;
+};
+
+Workspace layout(int tile, int D) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  Workspace w;
+  w.part_lse = up(static_cast<size_t>(2) * tree::kMaxWorkers * tile * D * 4);
+  w.cuts = w.part_lse + up(static_cast<size_t>(2) * tree::kMaxWorkers * tile * 4);
+  w.total = w.cuts + up(static_cast<size_t>(2) * tree::kMaxWorkers * sizeof(int4));
+  return w;
+}
+
+bool make_map(CUtensorMap* map, const fa_kv_cache& c, const void* base) {
+  host::EncodeTiledFn fn = host::encode_tiled_fn();
+  if (!fn) return false;
+  const CUtensorMapDataType dt = c.dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.H_kv), static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.row_stride) * 2, static_cast<cuuint64_t>(c.head_stride) * 2,
+                                 static_cast<cuuint64_t>(c.page_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(c.page_size < tree::kKeys ? c.page_size : tree::kKeys), 1, 1};
+  const cuuint32_t unit[4] = {1, 1, 1, 1};
+  return fn(map, dt, 4, const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16, int N>
+int launch_t(const TreeArgs& a, cudaStream_t stream) {
+  CUtensorMap tk, tv;
+  if (!make_map(&tk, a.cache, a.cache.k) || !make_map(&tv, a.cache, a.cache.v))
+    return static_cast<int>(cudaErrorInvalidValue);
+  const Workspace ws = layout(N, D);
+  uint8_t* base = static_cast<uint8_t*>(a.workspace);
+  tree::Params p{};
+  p.q = static_cast<const uint16_t*>(a.q.data);
+  p.o = static_cast<uint16_t*>(a.o.data);
+  p.lse = a.lse;
+  p.q_row = a.q.row_stride;
+  p.q_head = a.q.head_stride;
+  p.o_row = a.o.row_stride;
+  p.o_head = a.o.head_stride;
+  p.B = a.B;
+  p.rows = a.rows;
+  p.Hq = a.Hq;
+  p.H_kv = a.cache.H_kv;
+  p.G = a.Hq / a.cache.H_kv;
+  p.d = a.cache.d;
+  p.num_pages = a.cache.num_pages;
+  p.max_pages = a.max_pages;
+  p.page_shift = a.page_shift;
+  p.words = a.words;
+  p.block_table = a.block_table;
+  p.cu_q = a.cu_q;
+  p.seq_len = a.seq_len;
+  p.tree_mask = a.tree_mask;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.by_unit = by_unit(a.rows, a.max_q, a.Hq, a.cache.H_kv, N);
+  const int sms = host::sm_count();
+  p.workers = sms > 0 && sms < tree::kMaxWorkers ? sms : tree::kMaxWorkers;
+  p.part_o = reinterpret_cast<float*>(base);
+  p.part_lse = reinterpret_cast<float*>(base + ws.part_lse);
+  p.cuts = reinterpret_cast<int4*>(base + ws.cuts);
+  p.status = a.status;
+  p.timeout_ns = FA_WAIT_TIMEOUT_NS;
+
+  auto kern = tree::fa_tree_kernel<D, BF16, N>;
+  constexpr int kSmem = tree::Smem<D, N>::kAlloc;
+  cudaError_t e = host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  constexpr unsigned kThreads = 128 * tree::Smem<D, N>::kGroups + 64;
+  // By unit: request b has at most H_kv * (its rows / N rounded up) units.
+  const long long grid = p.by_unit ? static_cast<long long>(p.H_kv) *
+                                         ((static_cast<long long>(a.rows) * p.G + N - 1) / N + a.B)
+                                   : p.workers;
+  kern<<<static_cast<unsigned>(grid), kThreads, kSmem, stream>>>(tk, tv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.by_unit) return static_cast<int>(e);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.workers), N / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, tree::fa_tree_merge_kernel<D, BF16, N>, p));
+}
+
+template <int D, bool BF16>
+int launch_d(const TreeArgs& a, cudaStream_t stream) {
+  switch (row_tile(a.max_q, a.Hq / a.cache.H_kv)) {
+    case 16: return launch_t<D, BF16, 16>(a, stream);
+    case 32: return launch_t<D, BF16, 32>(a, stream);
+    case 64: return launch_t<D, BF16, 64>(a, stream);
+    default: return launch_t<D, BF16, 128>(a, stream);
+  }
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(32 * kWarps) fa_tree_simple_kernel(const TreeArgs p) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][256];
-  const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  int b = -1;
-  for (int k = 0; k < p.B; ++k)
-    if (p.cu_q[k] <= t && t < p.cu_q[k + 1]) {
-      b = k;
-      break;
-    }
-  if (b < 0) return;
-  const int d = p.cache.d, i = t - p.cu_q[b], n = p.cu_q[b + 1] - p.cu_q[b];
-  const int len = min(static_cast<long long>(p.seq_len[b]), static_cast<long long>(p.max_pages) << p.page_shift);
-  const int ctx = p.seq_len[b] - n, kvh = h / (p.Hq / p.cache.H_kv);
-  const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + t * p.q.row_stride + h * p.q.head_stride;
-  float qv[8], acc[8], m = -INFINITY, l = 0.0f;
-  for (int c = 0; c < d / 32; ++c) {
-    qv[c] = widen<BF16>(q[lane + 32 * c]) * p.scale;
-    acc[c] = 0.0f;
+int launch_type(const TreeArgs& a, cudaStream_t stream) {
+  switch (padded_dim(a.cache.d)) {
+    case 64: return launch_d<64, BF16>(a, stream);
+    case 128: return launch_d<128, BF16>(a, stream);
+    default: return launch_d<256, BF16>(a, stream);
   }
-  for (int j = warp; j < len; j += kWarps) {
-    bool seen = p.tree_mask == nullptr ? j <= i + ctx : j < ctx;
-    if (p.tree_mask != nullptr && j >= ctx && j - ctx < 64 * p.words)
-      seen = (p.tree_mask[static_cast<size_t>(t) * p.words + (j - ctx) / 64] >> ((j - ctx) % 64)) & 1;
-    const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + (j >> p.page_shift)];
-    if (!seen || page < 0 || page >= p.cache.num_pages) continue;
-    const long long off = page * p.cache.page_stride + kvh * p.cache.head_stride +
-                          (j & ((1 << p.page_shift) - 1)) * p.cache.row_stride;
-    const uint16_t* k = static_cast<const uint16_t*>(p.cache.k) + off;
-    const uint16_t* v = static_cast<const uint16_t*>(p.cache.v) + off;
-    float s = 0.0f;
-    for (int c = 0; c < d / 32; ++c) s = fmaf(qv[c], widen<BF16>(k[lane + 32 * c]), s);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float nm = fmaxf(m, s), a = m == -INFINITY ? 0.0f : expf(m - nm), e = expf(s - nm);
-    m = nm;
-    l = l * a + e;
-    for (int c = 0; c < d / 32; ++c) acc[c] = acc[c] * a + e * widen<BF16>(v[lane + 32 * c]);
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  for (int c = 0; c < d / 32; ++c) s_o[warp][lane + 32 * c] = acc[c];
-  __syncthreads();
-  float mx = -INFINITY, z = 0.0f;
-  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) z += s_m[w] == -INFINITY ? 0.0f : s_l[w] * expf(s_m[w] - mx);
-  for (int c = threadIdx.x; c < d; c += 32 * kWarps) {
-    float x = 0.0f;
-    for (int w = 0; w < kWarps; ++w) x += s_m[w] == -INFINITY ? 0.0f : s_o[w][c] * expf(s_m[w] - mx);
-    x = z > 0.0f ? x / z : 0.0f;
-    uint16_t* o = static_cast<uint16_t*>(p.o.data) + t * p.o.row_stride + h * p.o.head_stride + c;
-    if constexpr (BF16) *reinterpret_cast<__nv_bfloat16*>(o) = __float2bfloat16_rn(x);
-    else *reinterpret_cast<__half*>(o) = __float2half_rn(x);
-  }
-  if (threadIdx.x == 0) p.lse[static_cast<size_t>(t) * p.Hq + h] = z > 0.0f ? mx + logf(z) : -INFINITY;
 }
 
 }  // namespace
 
-size_t tree_fwd_workspace(int, int, int, int, int, int) { return 256; }
+size_t tree_fwd_workspace(int, int, int max_q, int Hq, int H_kv, int d) {
+  return layout(row_tile(max_q, Hq / H_kv), padded_dim(d)).total;
+}
 
 int launch_tree_fwd(const TreeArgs& a, cudaStream_t stream) {
-  if (a.rows == 0) return 0;
-  dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>(a.Hq));
-  if (a.cache.dtype == FA_BF16) fa_tree_simple_kernel<true><<<grid, 32 * kWarps, 0, stream>>>(a);
-  else fa_tree_simple_kernel<false><<<grid, 32 * kWarps, 0, stream>>>(a);
-  return static_cast<int>(cudaGetLastError());
+  return a.cache.dtype == FA_BF16 ? launch_type<true>(a, stream) : launch_type<false>(a, stream);
 }
 
 }  // namespace fa
