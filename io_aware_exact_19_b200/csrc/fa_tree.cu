@@ -7,10 +7,11 @@
 namespace fa {
 namespace {
 
-// Columns of the MMA: the smallest tile that holds a request's rows of one cache head.
-int row_tile(int max_q, int group) {
+// Columns of the MMA: the smallest tile that holds a request's rows of one cache head. With
+// head dimension 256 shared memory holds no more than 64 rows next to one stage of K and V.
+int row_tile(int max_q, int group, int D) {
   const long long rows = static_cast<long long>(max_q) * group;
-  return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 || D == 256 ? 64 : 128));
 }
 
 int padded_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
@@ -92,7 +93,7 @@ int launch_t(const TreeArgs& a, cudaStream_t stream) {
   constexpr int kSmem = tree::Smem<D, N>::kAlloc;
   cudaError_t e = host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  constexpr unsigned kThreads = 128 * tree::Smem<D, N>::kGroups + 64;
+  constexpr unsigned kThreads = 128 * tree::Smem<D, N>::kGroups + 96;
   // By unit: request b has at most H_kv * (its rows / N rounded up) units.
   const long long grid = p.by_unit ? static_cast<long long>(p.H_kv) *
                                          ((static_cast<long long>(a.rows) * p.G + N - 1) / N + a.B)
@@ -114,11 +115,11 @@ int launch_t(const TreeArgs& a, cudaStream_t stream) {
 
 template <int D, bool BF16>
 int launch_d(const TreeArgs& a, cudaStream_t stream) {
-  switch (row_tile(a.max_q, a.Hq / a.cache.H_kv)) {
+  switch (row_tile(a.max_q, a.Hq / a.cache.H_kv, D)) {
     case 16: return launch_t<D, BF16, 16>(a, stream);
     case 32: return launch_t<D, BF16, 32>(a, stream);
     case 64: return launch_t<D, BF16, 64>(a, stream);
-    default: return launch_t<D, BF16, 128>(a, stream);
+    default: return launch_t<D, BF16, D == 256 ? 64 : 128>(a, stream);
   }
 }
 
@@ -134,7 +135,7 @@ int launch_type(const TreeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t tree_fwd_workspace(int, int, int max_q, int Hq, int H_kv, int d) {
-  return layout(row_tile(max_q, Hq / H_kv), padded_dim(d)).total;
+  return layout(row_tile(max_q, Hq / H_kv, padded_dim(d)), padded_dim(d)).total;
 }
 
 int launch_tree_fwd(const TreeArgs& a, cudaStream_t stream) {

@@ -22,8 +22,8 @@
 // explainer, section 3.2, applied to runs of keys). Prompt chunks, whose units are many
 // and long, are not cut: a CTA per unit, the longest first.
 //
-// Warp roles: 4 (N <= 64) or 8 softmax warps (warpgroup w owns columns 64w .. 64w+63),
-// then a TMA producer warp, whose lanes each fetch pages of the tile, and an MMA warp.
+// Warp roles: a softmax warpgroup for every 32 columns (a thread holds its key's scores for
+// them), then a TMA producer warp for K, the MMA warp, and a producer warp for V.
 #pragma once
 
 #include "fa_cache.h"
@@ -84,37 +84,37 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
   return any != 0;
 }
 
-template <int D, int N>
-struct Smem {
-  static constexpr int kGroups = N == 128 ? 2 : 1;        // softmax warpgroups
-  static constexpr int kCols = N / kGroups;                // columns of a thread
-  static constexpr int kTile = kKeys * D * 2;              // one K or V tile
-  static constexpr int kChunk = kKeys * 128;               // its 64-column chunk
-  static constexpr int kQ = N * D * 2;
-  static constexpr int kP = kGroups * kKeys * 128;         // [group][key][64 columns]
-  static constexpr int kStages = D == 256 ? 1 : (D == 128 ? (N == 128 ? 2 : 3) : (N == 128 ? 5 : 6));
-  static constexpr int kQOff = 0;
-  static constexpr int kPOff = kQOff + (kQ + 1023) / 1024 * 1024;
-  static constexpr int kKOff = kPOff + kP;
-  static constexpr int kVOff = kKOff + kStages * kTile;
-  static constexpr int kRefOff = kVOff + kStages * kTile;  // minus the reference of each column
-  static constexpr int kBarOff = kRefOff + 4 * N;
-  // q_full, p_full, pv_done, drain, s_full[2], then k_full, k_empty, v_full, v_empty of each stage
-  static constexpr int kNumBars = 6 + 4 * kStages;
-  static constexpr int kMiscOff = kBarOff + 8 * kNumBars;  // TMEM base, abort flag, first request, its offset
-  static constexpr int kBytes = kMiscOff + 32;
-  static constexpr int kAlloc = kBytes + 1024;
-  static_assert(kAlloc <= 232448, "shared memory");
-  static_assert(4 * 4 * kCols + 8 * kCols <= kKeys * 128, "the reductions' scratch lies in P");
-};
-
 // A run of key tiles of one unit.
 struct Item {
+  int ctx;             // rows of the request before its new ones (seq_len - n; negative: not all are there)
   int b, q0, n, len;   // request, its first row, its rows, its keys
   int h, r0;           // cache head, first query row (token * G + head in group) of the unit
   int t0, t1;          // key tiles to visit
-  int whole;           // the unit is not cut
+  int clean;           // tiles before this one are seen whole by every row
   int take, tiles;     // tiles of this run and of the unit, before the causal reach
+  int valid;
+};
+
+// x / y, in 32 bits where they suffice.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
+}
+
+// `total` tiles in equal runs: worker w takes begin(w) .. begin(w + 1) - 1. Every worker up to
+// the total has one tile at least.
+struct Share {
+  long long base, more, total;
+  __device__ __forceinline__ void set(long long tiles, long long workers) {
+    const long long w = max(min(workers, tiles), 1ll);
+    total = tiles;
+    base = divide(tiles, w);
+    more = tiles - base * w;  // the first workers take one tile more
+  }
+  __device__ __forceinline__ long long begin(long long w) const { return min(w * base + min(w, more), total); }
+  __device__ __forceinline__ int worker(long long tile) const {
+    const long long long_runs = more * (base + 1);
+    return static_cast<int>(tile < long_runs ? divide(tile, base + 1) : more + divide(tile - long_runs, base));
+  }
 };
 
 // Walks the runs of a CTA. Units of request b: h-major over (cache head, N-row tile).
@@ -135,62 +135,113 @@ struct Cursor {
     return static_cast<long long>(p.H_kv) * units * tiles;
   }
 
-  __device__ __forceinline__ bool next(const Params& p, Item& it) {
+  // The item at the cursor, in request b whose rows, keys, units and tiles are given.
+  __device__ __forceinline__ void take(const Params& p, Item& it, int q0, int n, int len, int units, int tiles) {
+    const long long u = divide(off, tiles);
+    const int t = static_cast<int>(off - u * tiles);
+    const int h = static_cast<int>(divide(u, units));
+    int rt = static_cast<int>(u - static_cast<long long>(h) * units);
+    if (p.by_unit) rt = units - 1 - rt;  // under a chain the last rows see the most keys
+    const int r0 = rt * N, ctx = max(p.seq_len[b], 0) - n;
+    const int taken = static_cast<int>(min(static_cast<long long>(tiles - t), end - pos));
+    int t1 = (len + kKeys - 1) / kKeys;
+    if (!p.by_unit) t1 = min(t + taken, t1);
+    int whole_to = ctx;  // keys that every row sees
+    if (p.tree_mask == nullptr) {
+      // The chain's reach: the unit's last token sees keys up to its own. (seq_len may say
+      // more than the pages hold; the tokens' places follow seq_len.)
+      const int reach = ctx + min((r0 + N - 1) / p.G, n - 1) + 1;
+      t1 = min(t1, reach <= 0 ? 0 : (reach - 1) / kKeys + 1);
+      whole_to += r0 / p.G + 1;
+    }
+    it.ctx = ctx;
+    it.b = b;
+    it.q0 = q0;
+    it.n = n;
+    it.len = len;
+    it.h = h;
+    it.r0 = r0;
+    it.t0 = t;
+    it.t1 = max(t1, t);
+    it.clean = max(min(whole_to, len), 0) / kKeys;
+    it.take = taken;
+    it.tiles = tiles;
+    it.valid = 1;
+    pos += taken;
+    off += taken;
+  }
+
+  __device__ __forceinline__ void next(const Params& p, Item& it) {
+    it.valid = 0;
     while (pos < end && b < p.B) {
-      int units, tiles;
-      const long long w = weight(p, b, it.q0, it.n, it.len, units, tiles);
+      int q0, n, len, units, tiles;
+      const long long w = weight(p, b, q0, n, len, units, tiles);
       if (off >= w) {
         off -= w;
         ++b;
         continue;
       }
-      const unsigned long long u = static_cast<unsigned long long>(off) / static_cast<unsigned>(tiles);
-      const int t = static_cast<int>(off - static_cast<long long>(u) * tiles);
-      it.b = b;
-      it.h = static_cast<int>(u / static_cast<unsigned>(units));
-      int rt = static_cast<int>(u - static_cast<unsigned long long>(it.h) * units);
-      if (p.by_unit) rt = units - 1 - rt;  // under a chain the last rows see the most keys
-      it.r0 = rt * N;
-      it.take = static_cast<int>(min(static_cast<long long>(tiles - t), end - pos));
-      it.tiles = tiles;
-      it.whole = it.take == tiles;
-      it.t0 = t;
-      it.t1 = p.by_unit ? (it.len + kKeys - 1) / kKeys : min(t + it.take, (it.len + kKeys - 1) / kKeys);
-      if (p.tree_mask == nullptr) {
-        // The chain's reach: the unit's last token sees keys up to its own. (seq_len may say
-        // more than the pages hold; the tokens' places follow seq_len.)
-        const int last = min((it.r0 + N - 1) / p.G, it.n - 1);
-        const long long reach = static_cast<long long>(p.seq_len[b]) - it.n + last + 1;
-        const int lim = reach <= 0 ? 0 : static_cast<int>((reach + kKeys - 1) / kKeys);
-        it.t1 = min(it.t1, lim);
-      }
-      it.t1 = max(it.t1, it.t0);
-      pos += it.take;
-      off += it.take;
-      return true;
+      take(p, it, q0, n, len, units, tiles);
+      return;
     }
-    return false;
   }
 };
 
-// Reduce v[c] over the 32 lanes for each of C columns: lane l ends with columns
-// C/32 * l .. (C = 64: two, v[0] and v[1]; C = 32: one; C = 16: column l / 2).
+// Where the softmax warps stand, kept in shared memory rather than in every thread's registers:
+// their first thread walks on, an item ahead. Three slots: one warpgroup may still finish
+// item k while the walker, past the barrier behind item k's tiles, writes item k + 2.
+template <int N>
+struct Walk {
+  Cursor<N> cur;
+  long long unit_at[3];  // where the item's unit begins in the run of all tiles
+  Item item[3];
+};
+
+template <int D, int N>
+struct Smem {
+  static constexpr int kCols = N < 32 ? N : 32;            // columns of a softmax thread
+  static constexpr int kGroups = N / kCols;                // softmax warpgroups
+  static constexpr int kTile = kKeys * D * 2;              // one K or V tile
+  static constexpr int kChunk = kKeys * 128;               // its 64-column chunk
+  static constexpr int kQ = N * D * 2;
+  static constexpr int kP = (N == 128 ? 2 : 1) * (N >= 64 ? (D == 128 && N == 64 ? 1 : 2) : 1) * kKeys * 128;
+  // P of a tile while P V still reads the last one's: two buffers, of up to 32 columns side by
+  // side in one chunk; one where shared memory is better spent on a third stage of K and V.
+  static constexpr int kPBufs = D == 128 && N == 64 ? 1 : 2;
+  static constexpr int kPStep = N <= 32 ? 64 : (N == 128 ? 2 : 1) * kKeys * 128;  // bytes from one to the other
+  static constexpr int kStages = D == 256 ? 1 : (D == 128 ? (N == 128 ? 2 : 3) : (N == 128 ? 4 : (N == 64 ? 5 : 6)));
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = kQOff + (kQ + 1023) / 1024 * 1024;
+  static constexpr int kKOff = kPOff + kP;
+  static constexpr int kVOff = kKOff + kStages * kTile;
+  static constexpr int kRefOff = kVOff + kStages * kTile;  // minus the reference of each column
+  static constexpr int kRedOff = kRefOff + 4 * N;          // [group][4 warps][columns]
+  static constexpr int kWalkOff = kRedOff + 4 * 4 * N;
+  static constexpr int kBarOff = (kWalkOff + static_cast<int>(sizeof(Walk<N>)) + 7) / 8 * 8;
+  // q_full, drain, s_full[2], p_full[2], pv_done[2], then k_full, k_empty, v_full, v_empty of each stage
+  static constexpr int kNumBars = 8 + 4 * kStages;
+  static constexpr int kBadOff = kBarOff + 8 * kNumBars;   // [2 * stages] whether a tile has a bad page
+  static constexpr int kMiscOff = (kBadOff + 8 * kStages + 7) / 8 * 8;  // TMEM base, abort flag, first request, its offset
+  static constexpr int kFirstOff = kMiscOff + 16;           // the CTA's first run and where it goes on
+  static constexpr int kBytes = kFirstOff + static_cast<int>(sizeof(Cursor<N>) + sizeof(Item));
+  static constexpr int kAlloc = kBytes;
+  static_assert(kAlloc <= 232448, "shared memory");
+};
+
+// Reduce v[c] over the 32 lanes for each of C columns: lane l ends with column l (C = 32) or
+// l / 2 (C = 16) in v[0].
 template <int C, bool kMax>
 __device__ __forceinline__ void reduce_columns(float (&v)[C]) {
   const int lane = lane_id();
-  int cnt = C;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (cnt > 1) {
-      cnt >>= 1;
+  for (int o = 16, cnt = C / 2; o > 0; o >>= 1, cnt >>= 1) {
+    if (cnt > 0) {
       const bool up = lane & o;
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i) {
-        if (i < cnt) {
-          const float send = up ? v[i] : v[i + cnt], keep = up ? v[i + cnt] : v[i];
-          const float got = __shfl_xor_sync(0xffffffffu, send, o);
-          v[i] = kMax ? fmaxf(keep, got) : keep + got;
-        }
+      for (int i = 0; i < cnt; ++i) {
+        const float send = up ? v[i] : v[i + cnt], keep = up ? v[i + cnt] : v[i];
+        const float got = __shfl_xor_sync(0xffffffffu, send, o);
+        v[i] = kMax ? fmaxf(keep, got) : keep + got;
       }
     } else {
       const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
@@ -200,64 +251,75 @@ __device__ __forceinline__ void reduce_columns(float (&v)[C]) {
 }
 
 template <int C>
-__device__ __forceinline__ void store_columns(float* dst, const float (&v)[C]) {
-  const int lane = lane_id();
-  if constexpr (C == 64) {
-    dst[2 * lane] = v[0];
-    dst[2 * lane + 1] = v[1];
-  } else if constexpr (C == 32) {
-    dst[lane] = v[0];
-  } else {
-    if (lane % 2 == 0) dst[lane / 2] = v[0];
-  }
-}
-
-template <int C>
 __device__ __forceinline__ void load_scores(uint32_t t, float (&s)[C]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(s);
-  if constexpr (C == 16) {
-    tmem_ld16(t, *reinterpret_cast<uint32_t(*)[16]>(r));
-  } else {
-#pragma unroll
-    for (int c = 0; c < C; c += 32) tmem_ld32(t + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
-  }
+  if constexpr (C == 16) tmem_ld16(t, reinterpret_cast<uint32_t(&)[16]>(s));
+  else tmem_ld32(t, reinterpret_cast<uint32_t(&)[32]>(s));
   tmem_ld_wait();
 }
 
+// A softmax warp's wait. Its result does not matter: after one has run out, the abort flag
+// lets every later one return at once and the warp goes on through the same steps.
+__device__ __forceinline__ void wait_tile(uint32_t bar, uint32_t parity, const WaitCtx& ctx) {
+  mbar_wait(bar, parity, ctx);
+  __syncwarp();
+}
+
+// (a, b) * (s, s) + (c, d) in one instruction.
+__device__ __forceinline__ void fma2(float& a, float& b, float s, float c, float d) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %4};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(c), "f"(d));
+}
+
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
 template <int D, bool BF16, int N>
-__global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
+__global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                    const Params p) {
   using L = Smem<D, N>;
   constexpr int S = L::kStages, C = L::kCols, kSoftWarps = 4 * L::kGroups;
-  constexpr int kThreads = 128 * L::kGroups + 64;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kThreads = 128 * L::kGroups + 96;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the tiles' swizzle counts from 1024-byte boundaries
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  int* first_b = reinterpret_cast<int*>(smem + L::kMiscOff + 8);
-  long long* first_off = reinterpret_cast<long long*>(smem + L::kMiscOff + 16);
+  Cursor<N>* first_cur = reinterpret_cast<Cursor<N>*>(smem + L::kFirstOff);
+  Item* first_item = reinterpret_cast<Item*>(smem + L::kFirstOff + sizeof(Cursor<N>));
+  int* bad_page = reinterpret_cast<int*>(smem + L::kBadOff);
   float* minus_ref = reinterpret_cast<float*>(smem + L::kRefOff);
-  const uint32_t q_full = smem_u32(&bars[0]), p_full = smem_u32(&bars[1]), pv_done = smem_u32(&bars[2]),
-                 drain = smem_u32(&bars[3]);
-  auto s_full = [&](int i) { return smem_u32(&bars[4 + i]); };
-  auto k_full = [&](int s) { return smem_u32(&bars[6 + s]); };
-  auto k_empty = [&](int s) { return smem_u32(&bars[6 + S + s]); };
-  auto v_full = [&](int s) { return smem_u32(&bars[6 + 2 * S + s]); };
-  auto v_empty = [&](int s) { return smem_u32(&bars[6 + 3 * S + s]); };
+  const uint32_t q_full = smem_u32(&bars[0]), drain = smem_u32(&bars[1]);
+  // Of tile n, two of each: with two buffers of P a warpgroup may be a tile ahead of another.
+  auto s_full = [&](int n) { return smem_u32(&bars[2 + (n & 1)]); };
+  auto p_full = [&](int n) { return smem_u32(&bars[4 + (n & 1)]); };
+  auto pv_done = [&](int n) { return smem_u32(&bars[6 + (n & 1)]); };
+  auto k_full = [&](int s) { return smem_u32(&bars[8 + s]); };
+  auto k_empty = [&](int s) { return smem_u32(&bars[8 + S + s]); };
+  auto v_full = [&](int s) { return smem_u32(&bars[8 + 2 * S + s]); };
+  auto v_empty = [&](int s) { return smem_u32(&bars[8 + 3 * S + s]); };
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   constexpr uint32_t kTmemO = 256;  // O^T columns; S^T buffers at 0 and N
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     *abort_flag = 0;
-    *first_b = p.B;
-    mbar_init(q_full, 128 * L::kGroups);
-    mbar_init(p_full, 128 * L::kGroups);
-    mbar_init(pv_done, 1);
+    first_item->valid = 0;
+    first_cur->pos = first_cur->end = 0;
+    mbar_init(q_full, kSoftWarps);
     mbar_init(drain, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(s_full(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(p_full(i), kSoftWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(pv_done(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(s_full(i), 2);  // the commit, and the issuer (for what it has seen)
     for (int s = 0; s < S; ++s) {
       mbar_init(k_full(s), 1);
       mbar_init(k_empty(s), 1);
@@ -273,17 +335,18 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
   }
 
   // The CTA's run of tiles: sums of the requests' weights (kept in the ring, which is
-  // still empty), then the request in which the run begins.
-  long long lo, hi, workers, total = 0;
+  // still empty); the thread that has the request in which the run begins finds the first item.
+  long long lo, total = 0;
+  Share share;
   {
     long long* before = reinterpret_cast<long long*>(smem + L::kKOff);  // [B]
     long long* warp_sum = before + kCacheMaxB;
     constexpr int kWarps = kThreads / 32;
+    long long mine = 0, w = 0;  // of this thread's last request: the weights before it, its own
+    int q0 = 0, n = 0, len = 0, units = 1, tiles = 1;
     for (int base = 0; base < p.B; base += kThreads) {
       const int b = base + tid;
-      long long w = 0;
-      int q0, n, len, units, tiles;
-      if (b < p.B) w = Cursor<N>::weight(p, b, q0, n, len, units, tiles);
+      w = b < p.B ? Cursor<N>::weight(p, b, q0, n, len, units, tiles) : 0;
       long long s = w;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
@@ -292,24 +355,33 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
       }
       if (lane == 31) warp_sum[warp] = s;
       __syncthreads();
-      long long ahead = total;
+      mine = total + s - w;
       for (int i = 0; i < kWarps; ++i) {
         const long long x = warp_sum[i];
-        ahead += i < warp ? x : 0;
+        mine += i < warp ? x : 0;
         total += x;
       }
-      if (b < p.B) before[b] = ahead + s - w;
+      if (p.B > kThreads && b < p.B) before[b] = mine;
       __syncthreads();
     }
-    const long long me = blockIdx.x;
-    workers = min(static_cast<long long>(p.workers), max(total, 1ll));  // each has a tile at least
-    lo = p.by_unit ? me : min(me * total / workers, total);
-    hi = p.by_unit ? min(me + 1, total) : min((me + 1) * total / workers, total);
-    for (int b = tid; b < p.B; b += kThreads) {
-      const long long from = before[b], to = b + 1 < p.B ? before[b + 1] : total;
-      if (from <= lo && lo < to) {
-        *first_b = b;
-        *first_off = lo - from;
+    share.set(total, p.by_unit ? max(total, 1ll) : p.workers);
+    lo = share.begin(blockIdx.x);
+    const long long hi = share.begin(static_cast<long long>(blockIdx.x) + 1);
+    if (p.B <= kThreads) {
+      if (lo < hi && mine <= lo && lo < mine + w) {
+        Cursor<N> c{lo, hi, lo - mine, tid};
+        c.take(p, *first_item, q0, n, len, units, tiles);
+        *first_cur = c;
+      }
+    } else {
+      for (int b = tid; b < p.B && lo < hi; b += kThreads) {
+        const long long from = before[b], to = b + 1 < p.B ? before[b + 1] : total;
+        if (from <= lo && lo < to) {
+          Cursor<N> c{lo, hi, lo - from, b};
+          Cursor<N>::weight(p, b, q0, n, len, units, tiles);
+          c.take(p, *first_item, q0, n, len, units, tiles);
+          *first_cur = c;
+        }
       }
     }
   }
@@ -319,135 +391,152 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx ctx{abort_flag, p.status, p.timeout_ns};
-  Cursor<N> cur;
-  cur.pos = lo;
-  cur.end = hi;
-  cur.b = *first_b;
-  cur.off = cur.b < p.B ? *first_off : 0;
   // (The prefix sums in the ring are not read any more: the barrier above is behind every read.)
 
-  if (warp == kSoftWarps) {
-    // ------------------------------------------------------------ TMA producer
+  if (warp == kSoftWarps || warp == kSoftWarps + 2) {
+    // ------------------------------------------------------------ TMA producers: K, and V
+    // A copy takes about 80 cycles to issue whatever its size, so with small pages (16 rows:
+    // 32 copies a tile) one warp for both would be slower than the memory.
+    const bool is_v = warp != kSoftWarps;
+    const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+    const uint32_t ring = smem_u32(smem) + (is_v ? L::kVOff : L::kKOff);
+    const uint32_t full0 = is_v ? v_full(0) : k_full(0), empty0 = is_v ? v_empty(0) : k_empty(0);
     const int per_tile = p.page_shift >= 7 ? 1 : kKeys >> p.page_shift;  // pages of a tile
     const int box_rows = kKeys / per_tile;
     constexpr int kChunks = D / 64;
-    if (lane == 0) {
-      prefetch_tmap(&tmap_k);
-      prefetch_tmap(&tmap_v);
-    }
-    int n = 0, k_issued = 0, v_issued = 0;
+    if (lane == 0) prefetch_tmap(map);
+    int issued = 0, s = 0, ph = 1;
     bool ok = true;
-    Item it;
-    while (ok && cur.next(p, it)) {
+    Cursor<N> cur = *first_cur;
+    Item it = *first_item;
+    for (; ok && it.valid; cur.next(p, it)) {
       const int32_t* table = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
-      for (int t = it.t0; ok && t < it.t1; ++t, ++n) {
-        const int s = n % S;
-        const uint32_t ph = ((n / S) & 1) ^ 1;
-        // A lane's page; none (behind the length, or a bad index) is a page past the last, which TMA
-        // fills with zeros.
-        int page = p.num_pages, row = 0;
-        if (lane < per_tile) {
-          const long long key = static_cast<long long>(t) * kKeys + lane * box_rows;
-          if (key < it.len) {
-            page = table[key >> p.page_shift];
-            row = static_cast<int>(key & ((1 << p.page_shift) - 1));
-            if (page < 0 || page >= p.num_pages) page = p.num_pages;
-          }
+      const int head = __shfl_sync(0xffffffffu, it.h, 0);
+      // A lane's page of tile t; none (behind the length, or a bad index) is a page past the last,
+      // which TMA fills with zeros.
+      auto page_of = [&](int t) {
+        const long long key = static_cast<long long>(t) * kKeys + lane * box_rows;
+        return lane < per_tile && key < it.len ? table[key >> p.page_shift] : p.num_pages;
+      };
+      int ahead = it.t0 < it.t1 ? page_of(it.t0) : 0;
+      for (int t = it.t0; t < it.t1; ++t) {
+        int page = ahead;
+        if (t + 1 < it.t1) ahead = page_of(t + 1);
+        const int first_row = per_tile == 1 ? (t * kKeys) & ((1 << p.page_shift) - 1) : 0;
+        bool bad = page < 0 || page >= p.num_pages;
+        if (bad) page = p.num_pages;
+        bad = __any_sync(0xffffffffu, bad && lane < per_tile && static_cast<long long>(t) * kKeys + lane * box_rows < it.len);
+        if (!(ok = mbar_wait_warp(empty0 + 8 * s, ph, ctx))) break;
+        if (lane == 0) {
+          // Twice the stages: the softmax may still look at the tile whose K this one replaces.
+          if (!is_v) bad_page[issued % (2 * S)] = bad;
+          mbar_arrive_expect_tx(full0 + 8 * s, L::kTile);
         }
-        auto fetch = [&](const CUtensorMap* map, uint32_t full, int ring) {
-          if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
-          __syncwarp();
-          if (lane < per_tile) {
-            const uint32_t dst = smem_u32(smem + ring + s * L::kTile) + lane * box_rows * 128;
+        __syncwarp();
+        // One elected lane issues every page's boxes: their operands are then the same in all lanes.
+        for (int i = 0; i < per_tile; ++i) {
+          const int pg = __shfl_sync(0xffffffffu, page, i);
+          if (elect_one()) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-              tma_load_4d(dst + c * L::kChunk, map, full, c * 64, row, it.h, page);
+              tma_load_4d(ring + s * L::kTile + i * box_rows * 128 + c * L::kChunk, map, full0 + 8 * s, c * 64, first_row,
+                          head, pg);
           }
-          __syncwarp();
-        };
-        if (!(ok = mbar_wait_warp(k_empty(s), ph, ctx))) break;
-        fetch(&tmap_k, k_full(s), L::kKOff);
-        ++k_issued;
-        if (!(ok = mbar_wait_warp(v_empty(s), ph, ctx))) break;
-        fetch(&tmap_v, v_full(s), L::kVOff);
-        ++v_issued;
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == S) {
+          s = 0;
+          ph ^= 1;
+        }
       }
     }
     if (*abort_flag) {
       // Aborting: what is in flight lands before the CTA exits; the last load into a stage
       // completes that stage's phase.
-      for (int s = 0; s < S; ++s) {
-        if (k_issued > s)
-          mbar_wait_bounded(k_full(s), ((k_issued - 1 - (k_issued - 1 - s) % S) / S) & 1, kDrainNs);
-        if (v_issued > s)
-          mbar_wait_bounded(v_full(s), ((v_issued - 1 - (v_issued - 1 - s) % S) / S) & 1, kDrainNs);
-      }
+      for (int i = 0; i < S; ++i)
+        if (issued > i) mbar_wait_bounded(full0 + 8 * i, ((issued - 1 - (issued - 1 - i) % S) / S) & 1, kDrainNs);
     }
   } else if (warp == kSoftWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16(BF16, kKeys, N, false, false);
-      constexpr int kM = D == 64 ? 64 : 128;
-      constexpr uint32_t idesc_o = idesc_f16(BF16, kM, N, true, true);
-      const uint64_t dQ = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
-      const uint64_t dK = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
-      const uint64_t dV = sdesc_sw128(smem_u32(smem + L::kVOff), L::kChunk, 1024);
-      const uint64_t dP = sdesc_sw128(smem_u32(smem + L::kPOff), kKeys * 128, 1024);
-      auto issue_s = [&](int n) {
-        const int s = n % S;
-        const uint64_t a = sdesc_add(dK, static_cast<uint32_t>(s) * L::kTile);
+    // The whole warp walks and waits; one elected lane issues, so the operands of each MMA are
+    // the same in all lanes and sit in uniform registers.
+    constexpr uint32_t idesc_s = idesc_f16(BF16, kKeys, N, false, false);
+    constexpr int kM = D == 64 ? 64 : 128;
+    constexpr uint32_t idesc_o = idesc_f16(BF16, kM, N, true, true);
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
+    const uint64_t dK = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
+    const uint64_t dV = sdesc_sw128(smem_u32(smem + L::kVOff), L::kChunk, 1024);
+    const uint64_t dP = sdesc_sw128(smem_u32(smem + L::kPOff), kKeys * 128, 1024);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto issue_s = [&](int n, int s) {
+      const uint64_t a = sdesc_add(dK, static_cast<uint32_t>(s) * L::kTile);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t in = (k % 4) * 32;
-          umma_ss(tmem + (n & 1) * N, sdesc_add(a, (k / 4) * L::kChunk + in), sdesc_add(dQ, (k / 4) * N * 128 + in),
+          umma_ss(tm + (n & 1) * N, sdesc_add(a, (k / 4) * L::kChunk + in), sdesc_add(dQ, (k / 4) * N * 128 + in),
                   idesc_s, k > 0);
         }
-        umma_commit(s_full(n & 1));
+        umma_commit(s_full(n));
         umma_commit(k_empty(s));
-      };
-      auto issue_o = [&](int n, bool first) {
-        const uint64_t a = sdesc_add(dV, static_cast<uint32_t>(n % S) * L::kTile);
+        mbar_arrive(s_full(n));
+      }
+      __syncwarp();
+    };
+    auto issue_o = [&](int n, int s, uint32_t add) {
+      const uint64_t a = sdesc_add(dV, static_cast<uint32_t>(s) * L::kTile);
+      const uint64_t b = sdesc_add(dP, static_cast<uint32_t>(n % L::kPBufs) * L::kPStep);
+      if (elect_one()) {
 #pragma unroll
         for (int half = 0; half < (D == 256 ? 2 : 1); ++half)
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            umma_ss(tmem + kTmemO + half * N, sdesc_add(a, half * 2 * L::kChunk + k * 2048), sdesc_add(dP, k * 2048),
-                    idesc_o, !first || k > 0);
-        umma_commit(pv_done);
-        umma_commit(v_empty(n % S));
-      };
-      int n = 0, q_count = 0;
-      bool ok = true, issued = false;
-      Item it;
-      while (ok && cur.next(p, it)) {
-        const int tiles = it.t1 - it.t0;
-        if (tiles == 0) continue;
-        if (!(ok = mbar_wait(q_full, q_count & 1, ctx))) break;
-        ++q_count;
-        if (!(ok = mbar_wait(k_full(n % S), (n / S) & 1, ctx))) break;
-        tc_fence_after();
-        issue_s(n);
-        issued = true;
-        for (int j = 0; j < tiles; ++j, ++n) {
-          if (j + 1 < tiles) {
-            // The other S buffer was read before P of tile n - 1 arrived.
-            if (!(ok = mbar_wait(k_full((n + 1) % S), ((n + 1) / S) & 1, ctx))) break;
-            tc_fence_after();
-            issue_s(n + 1);
-          }
-          if (!(ok = mbar_wait(v_full(n % S), (n / S) & 1, ctx))) break;
-          if (!(ok = mbar_wait(p_full, n & 1, ctx))) break;
-          tc_fence_after();
-          issue_o(n, j == 0);
-        }
+            umma_ss(tm + kTmemO + half * N, sdesc_add(a, half * 2 * L::kChunk + k * 2048), sdesc_add(b, k * 2048),
+                    idesc_o, k > 0 ? 1u : add);
+        umma_commit(pv_done(n));
+        umma_commit(v_empty(s));
       }
-      if (!ok && issued) {
-        // Aborting: everything issued completes before TMEM and the operands go.
+      __syncwarp();
+    };
+    int n = 0, q_count = 0;
+    int s = 0, ph = 0;            // stage and phase of tile n
+    bool ok = true, issued = false;
+    Cursor<N> cur = *first_cur;
+    Item it = *first_item;
+    for (; ok && it.valid; cur.next(p, it)) {
+      const int tiles = __shfl_sync(0xffffffffu, it.t1 - it.t0, 0);
+      if (tiles == 0) continue;
+      if (!(ok = mbar_wait_warp(q_full, q_count & 1, ctx))) break;
+      ++q_count;
+      if (!(ok = mbar_wait_warp(k_full(s), ph, ctx))) break;
+      tc_fence_after();
+      issue_s(n, s);
+      issued = true;
+      for (int j = 0; j < tiles; ++j, ++n) {
+        const int s1 = s + 1 == S ? 0 : s + 1, ph1 = s + 1 == S ? ph ^ 1 : ph;
+        if (j + 1 < tiles) {
+          // The other S buffer was read before P of tile n - 1 arrived.
+          if (!(ok = mbar_wait_warp(k_full(s1), ph1, ctx))) break;
+          tc_fence_after();
+          issue_s(n + 1, s1);
+        }
+        if (!(ok = mbar_wait_warp(v_full(s), ph, ctx))) break;
+        if (!(ok = mbar_wait_warp(p_full(n), (n >> 1) & 1, ctx))) break;
+        tc_fence_after();
+        issue_o(n, s, j > 0);
+        s = s1;
+        ph = ph1;
+      }
+    }
+    if (!ok && issued) {
+      // Aborting: everything issued completes before TMEM and the operands go.
+      if (elect_one()) {
         umma_commit(drain);
         mbar_wait_bounded(drain, 0, kDrainNs);
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     // After a wait ran out every later one returns at once (the abort flag), and the
@@ -460,10 +549,11 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
     // small ones stay in its normal range: 2^7 * 2^8 < 65504).
     constexpr float kBias = BF16 ? 0.0f : 7.0f;
     float* ref = minus_ref + col0;
-    uint8_t* sP = smem + L::kPOff + group * (kKeys * 128);
-    float* red = reinterpret_cast<float*>(sP);       // [4][C], then
-    float* factor = red + 4 * C;                      // [C]
-    const uint32_t p_row = smem_u32(sP) + r * 128;
+    float* red = reinterpret_cast<float*>(smem + L::kRedOff) + group * 4 * C;  // [4][C]
+    float* factor = red;  // [C], each written over the column by the thread that has read it
+    // Row r of P: the group's half of its 64-column chunk, 16-byte pieces swizzled.
+    const uint32_t p_row = smem_u32(smem + L::kPOff) + (group / 2) * (kKeys * 128) + r * 128;
+    const int piece0 = (group % 2) * 4;
     int n = 0;          // tiles seen
     float l[C];
 
@@ -472,6 +562,7 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
       // columns past d are zero.
       constexpr int kVecs = N * D / 8;
       const int rows = it.n * p.G - it.r0;
+#pragma unroll 2
       for (int v = tid; v < kVecs; v += 128 * L::kGroups) {
         const int row = v / (D / 8), c = v % (D / 8);
         uint4 x = make_uint4(0, 0, 0, 0);
@@ -483,56 +574,86 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
                x.w);
       }
       fence_proxy_async_smem();
-      mbar_arrive(q_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
     };
 
-    Item it, following;
-    bool have = cur.next(p, it);
-    if (have && it.t1 > it.t0) load_q(it);
-    int4 cut0 = make_int4(0, 0, 0, 0), cut1 = cut0;
-    while (have) {
-      const long long unit_at = cur.pos - it.take - it.t0;  // where the unit begins in the run of all tiles
-      const bool more = cur.next(p, following);
-      const long long ctx_len = static_cast<long long>(p.seq_len[it.b]) - it.n;
-      const int32_t* table = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
+    Walk<N>& walk = *reinterpret_cast<Walk<N>*>(smem + L::kWalkOff);
+    auto soft_barrier = [] { asm volatile("bar.sync 8, %0;" ::"n"(128 * L::kGroups) : "memory"); };
+    auto advance = [&](int to) {
+      Item& it = walk.item[to];
+      walk.cur.next(p, it);
+      walk.unit_at[to] = walk.cur.pos - it.take - it.t0;
+    };
+    if (tid == 0) {
+      walk.cur = *first_cur;
+      walk.item[0] = *first_item;
+      walk.unit_at[0] = walk.cur.pos - walk.item[0].take - walk.item[0].t0;
+    }
+    soft_barrier();
+    if (walk.item[0].valid && walk.item[0].t1 > walk.item[0].t0) load_q(walk.item[0]);
+    int which = 0, then = 1;
+    if (gt == 0 && group == 0 && !p.by_unit) p.cuts[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    while (walk.item[which].valid) {
+      const Item& it = walk.item[which];
+      const int t1 = it.t1, len = it.len;
+      if (tid == 0) advance(then);
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] = 0.0f;
       const int n_first = n;
-      auto page_of = [&](int t) {
-        const long long key = static_cast<long long>(t) * kKeys + r;
-        return key < it.len ? table[key >> p.page_shift] : -1;
-      };
-      int page = it.t1 > it.t0 ? page_of(it.t0) : 0;
-      for (int t = it.t0; t < it.t1; ++t, ++n) {
-        const long long key = static_cast<long long>(t) * kKeys + r;
-        const bool alive = page >= 0 && page < p.num_pages;  // key < len included
-        if (t + 1 < it.t1) page = page_of(t + 1);
+      const int clean = it.clean;
+      for (int t = it.t0; t < t1; ++t, ++n) {
+        const int key = t * kKeys + r;
         // Columns that see this thread's key (bit c: column col0 + c).
-        unsigned long long seen = alive ? ~0ull : 0ull;
-        const long long own = key - ctx_len;  // its index among the new tokens
+        uint32_t seen = ~0u;
+        if (t >= clean) {
+        const bool alive = key < len;
+        seen = alive ? ~0u : 0u;
+        const long long own = key - it.ctx;  // its index among the new tokens
         const int first_row = it.r0 + col0;
-        if (alive && own >= 0) {
-          if (p.tree_mask == nullptr) {
+        if (p.tree_mask == nullptr) {
+          if (alive && own >= 0) {
             const long long c = own * p.G - first_row;  // rows of token `own` and later
-            seen = c <= 0 ? ~0ull : (c >= 64 ? 0ull : ~0ull << c);
-          } else {
-            seen = 0ull;
-            const int last = min((first_row + C - 1) / p.G, it.n - 1);
-            if (own < 64ll * p.words) {
-              const unsigned long long* m = p.tree_mask + static_cast<size_t>(it.q0) * p.words + own / 64;
-#pragma unroll 4
-              for (int tok = first_row / p.G; tok <= last; ++tok) {
-                const unsigned long long bit = (m[static_cast<size_t>(tok) * p.words] >> (own % 64)) & 1ull;
-                const int from = max(tok * p.G - first_row, 0), to = min((tok + 1) * p.G - first_row, 64);
-                if (bit) seen |= (~0ull >> (64 - to)) & (~0ull << from);  // its group's columns; 0 <= from < to
-              }
+            seen = c <= 0 ? ~0u : (c >= 32 ? 0u : ~0u << c);
+          }
+        } else if (own - lane + 31 >= 0) {
+          // Lane i fetches the bits of token first + i for the warp's 32 keys; then each key
+          // collects its bit of every token.
+          const int first = first_row / p.G, last = min((first_row + C - 1) / p.G, it.n - 1);
+          const long long base = own - lane;  // of the warp's first key; the context's keys are seen
+          uint32_t bits = 0;
+          if (first + lane <= last) {
+            const unsigned long long* m = p.tree_mask + static_cast<size_t>(it.q0 + first + lane) * p.words;
+            auto word = [&](long long i) { return i >= 0 && i < p.words ? m[i] : 0ull; };
+            if (base < 0) {
+              bits = ~0u >> (32 + base) | static_cast<uint32_t>(word(0) << -base);
+            } else {
+              const long long w = base / 64;
+              const int at = static_cast<int>(base % 64);
+              bits = static_cast<uint32_t>(word(w) >> at);
+              if (at > 32) bits |= static_cast<uint32_t>(word(w + 1) << (64 - at));
             }
           }
+          uint32_t mine = 0;
+          for (int tok = first; tok <= last; ++tok) {
+            const uint32_t b = __shfl_sync(0xffffffffu, bits, tok - first);
+            const int from = max(tok * p.G - first_row, 0), to = min((tok + 1) * p.G - first_row, 32);
+            if ((b >> lane) & 1u) mine |= (~0u >> (32 - to)) & (~0u << from);  // 0 <= from < to
+          }
+          if (alive) seen = mine;
         }
-        const bool masked = __any_sync(0xffffffffu, seen != ~0ull);
-
-        mbar_wait_warp(s_full(n & 1), (n >> 1) & 1, ctx);
+        }
+        wait_tile(s_full(n), (n >> 1) & 1, ctx);
         tc_fence_after();
+        bool masked = t >= clean;
+        if (bad_page[n % (2 * S)]) {
+          // A page index outside the cache: its keys are not there.
+          masked = true;
+          if (key < len) {
+            const int page = p.block_table[static_cast<size_t>(it.b) * p.max_pages + (key >> p.page_shift)];
+            if (page < 0 || page >= p.num_pages) seen = 0u;
+          }
+        }
         const uint32_t t_s = tmem + lanes + (n & 1) * N + col0;
         float x[C];
         load_scores<C>(t_s, x);
@@ -540,33 +661,39 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
             const float4 f = lds128(smem_u32(ref + c));
-            x[c] = fmaf(x[c], sl2, f.x);
-            x[c + 1] = fmaf(x[c + 1], sl2, f.y);
-            x[c + 2] = fmaf(x[c + 2], sl2, f.z);
-            x[c + 3] = fmaf(x[c + 3], sl2, f.w);
+            fma2(x[c], x[c + 1], sl2, f.x, f.y);
+            fma2(x[c + 2], x[c + 3], sl2, f.z, f.w);
           }
           if (masked) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
-              if (!((seen >> c) & 1ull)) x[c] = -INFINITY;
+              if (!((seen >> c) & 1u)) x[c] = -INFINITY;
           }
         };
-        against_ref();
-        float top = x[0];
+        const bool first = n == n_first;
+        bool move = first;
+        if (!first) {
+          against_ref();
+          float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 1; c < C; ++c) top = fmaxf(top, x[c]);
-        if (group_any(bar_id, top > kRescale + kBias)) {
-          // Some column's reference moves. P V of the tile before must be complete: it adds to O,
-          // and the scratch lies where it reads P.
-          if (n > n_first) {
-            mbar_wait_warp(pv_done, (n - 1) & 1, ctx);
-            tc_fence_after();
+          for (int c = 4; c < C; c += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[c + i]);
           }
-          load_scores<C>(t_s, x);
+          move = group_any(bar_id, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kRescale + kBias);
+        }
+        if (move) {
+          // Some column's reference moves (or is set, by the run's first tile). P V of the tile
+          // before, which adds to O, must be complete.
+          if (!first) {
+            wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
+            tc_fence_after();
+            load_scores<C>(t_s, x);
+          }
 #pragma unroll
-          for (int c = 0; c < C; ++c) x[c] = ((seen >> c) & 1ull) ? x[c] * sl2 : -INFINITY;
+          for (int c = 0; c < C; ++c) x[c] = ((seen >> c) & 1u) ? x[c] * sl2 : -INFINITY;
           reduce_columns<C, true>(x);
-          store_columns<C>(red + quarter * C, x);
+          red[quarter * C + (C == 32 ? lane : lane / 2)] = x[0];
           group_barrier(bar_id);
           if (gt < C) {
             const float high = fmaxf(fmaxf(red[gt], red[C + gt]), fmaxf(red[2 * C + gt], red[3 * C + gt])) - kBias;
@@ -576,11 +703,11 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
             ref[gt] = -now;
           }
           group_barrier(bar_id);
-          if (n > n_first) {
-#pragma unroll
-            for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
-              const uint32_t t_o = tmem + lanes + kTmemO + half * N + col0;
-#pragma unroll
+          if (!first) {
+#pragma unroll 1
+            for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {
+              const uint32_t t_o = tmem + lanes + kTmemO + h * N + col0;
+#pragma unroll 1
               for (int c = 0; c < C; c += 16) {
                 uint32_t o[16];
                 tmem_ld16(t_o + c, o);
@@ -591,29 +718,33 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
               }
             }
             tmem_st_wait();
-          }
 #pragma unroll
-          for (int c = 0; c < C; ++c) l[c] *= factor[c];
+            for (int c = 0; c < C; ++c) l[c] *= factor[c];
+          }
           load_scores<C>(t_s, x);
           against_ref();
-          group_barrier(bar_id);  // the scratch is read; P may be written
         }
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
+        for (int c = 0; c < C; c += 2) {
           x[c] = ex2(x[c]);
-          l[c] += x[c];
+          x[c + 1] = ex2(x[c + 1]);
+          add2(l[c], l[c + 1], x[c], x[c + 1]);
         }
-        // P V of the tile before has read its P.
-        if (n > n_first) mbar_wait_warp(pv_done, (n - 1) & 1, ctx);
+        // P V that read this buffer of P last is complete: with two buffers that of tile n - 2, which
+        // was issued before S of this tile, whose commit covers it.
+        if (L::kPBufs == 1 && !first) wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
+        const int buf = n % L::kPBufs;
+        const uint32_t p_at = p_row + (N <= 32 ? 0 : buf * L::kPStep);
+        const int piece = piece0 + (N <= 32 ? 4 * buf : 0);
 #pragma unroll
         for (int c = 0; c < C; c += 8)
-          sts128(p_row + (((c / 8) ^ (r % 8)) * 16), pack2<BF16>(x[c], x[c + 1]), pack2<BF16>(x[c + 2], x[c + 3]),
-                 pack2<BF16>(x[c + 4], x[c + 5]), pack2<BF16>(x[c + 6], x[c + 7]));
-        if (static_cast<long long>(t + 1) * kKeys > it.len) {
+          sts128(p_at + (((piece + c / 8) ^ (r % 8)) * 16), pack2<BF16>(x[c], x[c + 1]),
+                 pack2<BF16>(x[c + 2], x[c + 3]), pack2<BF16>(x[c + 4], x[c + 5]), pack2<BF16>(x[c + 6], x[c + 7]));
+        if (t >= clean && t * kKeys + (kKeys - 1) >= len) {
           // The last tile: what the page holds behind the last key may be anything, and 0 * NaN is
           // not 0, so those rows of V are cleared.
-          mbar_wait_warp(v_full(n % S), (n / S) & 1, ctx);
-          if (key >= it.len && group == 0) {
+          wait_tile(v_full(n % S), (n / S) & 1, ctx);
+          if (key >= len && group == 0) {
             const uint32_t row = smem_u32(smem + L::kVOff + (n % S) * L::kTile) + r * 128;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
@@ -623,20 +754,24 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(n));
       }
       // Every S of this unit is read, so Q may be replaced.
-      if (more && following.t1 > following.t0) load_q(following);
+      soft_barrier();  // every warp is done with them, and the item that follows is known
+      if (walk.item[then].valid && walk.item[then].t1 > walk.item[then].t0) load_q(walk.item[then]);
 
       // ---------------------------------------------------------- the run's result
       const bool some = n > n_first;
       if (some) {
-        mbar_wait_warp(pv_done, (n - 1) & 1, ctx);
+        wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
         tc_fence_after();
       }
       reduce_columns<C, false>(l);
-      store_columns<C>(red + quarter * C, l);
+      red[quarter * C + (C == 32 ? lane : lane / 2)] = l[0];
       group_barrier(bar_id);
+      const bool whole = it.take == it.tiles;
+      const long long unit_at = walk.unit_at[which];
       const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_at > lo ? 1 : 0);
       const int left = it.n * p.G - it.r0 - col0;  // columns of this group that are rows
       if (gt < C) {
@@ -644,7 +779,7 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
         const float lse2 = sum > 0.0f ? lg2(sum) - ref[gt] : (sum == 0.0f ? -INFINITY : sum);
         factor[gt] = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // NaN stays
         ref[gt] = kNoKey;
-        if (it.whole) {
+        if (whole) {
           if (gt < left) {
             const int rr = it.r0 + col0 + gt, tok = rr / p.G;
             p.lse[static_cast<size_t>(it.q0 + tok) * p.Hq + it.h * p.G + rr - tok * p.G] = lse2 * 0.6931471805599453f;
@@ -654,14 +789,14 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
         }
       }
       group_barrier(bar_id);
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
         const uint32_t t_o = tmem + lanes + kTmemO + half * N + col0;
         // M = 64 keeps row i in lane 32 * (i / 16) + i % 16.
         const int e = D == 64 ? quarter * 16 + lane : half * 128 + r;
         const bool mine = (D != 64 || lane < 16) && e < p.d;
         int tok = (it.r0 + col0) / p.G, g = (it.r0 + col0) - tok * p.G;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < C; c += 16) {
           uint32_t o[16];
           if (some) {
@@ -672,7 +807,7 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
           for (int i = 0; i < 16; ++i) {
             const float f = factor[c + i];
             const float y = some ? (f == 0.0f ? 0.0f : __uint_as_float(o[i]) * f) : 0.0f;
-            if (it.whole) {
+            if (whole) {
               if (mine && c + i < left)
                 p.o[(it.q0 + tok) * p.o_row + (it.h * p.G + g) * p.o_head + e] =
                     static_cast<uint16_t>(pack2<BF16>(y, 0.0f));
@@ -687,19 +822,14 @@ __global__ void __launch_bounds__(128 * (N == 128 ? 2 : 1) + 64, 1)
         }
       }
       tc_fence_before();
-      // The unit that goes on in the next CTAs: what the merge needs to know.
-      if (!it.whole && it.t0 == 0) {
-        const long long last = (unit_at + it.tiles) * workers;  // rounded up: the last worker with a tile of it
-        cut0 = make_int4(1, slot, static_cast<int>((last + total - 1) / total) - 1, it.q0);
-        cut1 = make_int4(it.h, it.r0, it.n, 0);
+      // The unit that goes on in the next CTAs (at most the last one): what the merge needs to know.
+      if (!whole && it.t0 == 0 && gt == 0 && group == 0) {
+        p.cuts[2 * blockIdx.x] = make_int4(1, slot, share.worker(unit_at + it.tiles - 1), it.q0);
+        p.cuts[2 * blockIdx.x + 1] = make_int4(it.h, it.r0, it.n, 0);
       }
-      group_barrier(bar_id);  // factor is read; the scratch may become P again
-      it = following;
-      have = more;
-    }
-    if (tid == 0 && !p.by_unit) {
-      p.cuts[2 * blockIdx.x] = cut0;
-      p.cuts[2 * blockIdx.x + 1] = cut1;
+      group_barrier(bar_id);  // the scratch is read
+      which = then;
+      then = then == 2 ? 0 : then + 1;
     }
   }
 
@@ -725,6 +855,8 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const Params p) {
   if (rr >= u.z * p.G) return;
   const int pieces = a.z - w + 1;
   auto slot_of = [&](int i) { return i == 0 ? a.y : 2 * (w + i); };
+  // Largest piece, then each piece's weight, 32 at a time, a lane each; the rows' loads do not
+  // depend on one another.
   float m = -INFINITY;
   bool nan = false;
   for (int i = lane; i < pieces; i += 32) {
@@ -740,18 +872,21 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const Params p) {
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
   if (m != -INFINITY || nan) {
-    for (int i = 0; i < pieces; ++i) {
-      const size_t row = static_cast<size_t>(slot_of(i)) * N + c;
-      const float x = p.part_lse[row];
-      if (x == -INFINITY) continue;
-      const float f = ex2(x - m);
-      z += f;
-      const float* src = p.part_o + row * D + lane * kPer;
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+      const float x = i0 + lane < pieces ? p.part_lse[static_cast<size_t>(slot_of(i0 + lane)) * N + c] : -INFINITY;
+      const float weight = x == -INFINITY ? 0.0f : ex2(x - m);
+      const int here = min(32, pieces - i0);
+#pragma unroll 4
+      for (int i = 0; i < here; ++i) {
+        const float f = __shfl_sync(0xffffffffu, weight, i);
+        z += f;
+        const float* src = p.part_o + (static_cast<size_t>(slot_of(i0 + i)) * N + c) * D + lane * kPer;
 #pragma unroll
-      for (int k = 0; k < kPer; k += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src + k);
-        acc[k] = fmaf(f, y.x, acc[k]);
-        acc[k + 1] = fmaf(f, y.y, acc[k + 1]);
+        for (int k = 0; k < kPer; k += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src + k);
+          acc[k] = fmaf(f, y.x, acc[k]);
+          acc[k + 1] = fmaf(f, y.y, acc[k + 1]);
+        }
       }
     }
   }
