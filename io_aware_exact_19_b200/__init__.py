@@ -34,20 +34,17 @@ EXPORTED = (
     "fa_cache_plan", "fa_rope", "fa_rope_append", "fa_tree_fwd", "fa_tree_fwd_workspace_size", "fa_cache_commit",
 )
 
-TREE_MAX = 512  # FA_TREE_MAX: tokens of a drafted tree
+# The paged cache's functions live in paged.py, which imports torch; they load on first use.
+_PAGED = ("fa_cache_plan", "fa_rope", "fa_rope_append", "fa_tree_fwd", "fa_tree_fwd_workspace_size", "fa_cache_commit",
+          "KVCacheDesc", "RowsDesc", "TREE_MAX")
 
 
-class KVCacheDesc(ctypes.Structure):
-    """fa_kv_cache of include/fa.h."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int),
-                ("page_size", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int),
-                ("page_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
-                ("row_stride", ctypes.c_longlong)]
-
-
-class RowsDesc(ctypes.Structure):
-    """fa_rows of include/fa.h."""
-    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+def __getattr__(name):
+    if name in _PAGED:
+        from . import paged
+        globals().update({n: getattr(paged, n) for n in _PAGED})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class FAError(RuntimeError):
@@ -391,196 +388,6 @@ def fa_debug_dropout_draws(B: int, H: int, Nq: int, Nk: int, seed: int, row_majo
     st = load_library().fa_debug_dropout_draws(B, H, Nq, Nk, ctypes.c_ulonglong(int(seed)), _ptr(row_major),
                                                _ptr(col_major), _stream(stream))
     _check(st, "fa_debug_dropout_draws")
-
-
-# ----------------------------------------------------------------------------- paged cache
-
-def _call(where: str, device, stream, *args) -> None:
-    """Call entry point ``where`` with the stream behind ``args``, on ``device``."""
-    import torch
-    lib = _lib or load_library()
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(where, device, stream, *args)
-    handle = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
-    _check(getattr(lib, where)(*args, handle), where)
-
-
-def _ints(device, dtype, **tensors):
-    """Contiguous integer tensors of one type on ``device``; the addresses in order."""
-    out = []
-    for name, t in tensors.items():
-        if t.dtype != dtype or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name}: expected a contiguous {dtype} tensor on {device}, got {t.dtype} on {t.device}")
-        out.append(t.data_ptr())
-    return out
-
-
-def _strides(t):
-    """Element strides of all but the last dimension (a dimension of size 1 has none of its own)."""
-    d = t.shape[-1]
-    if d > 1 and t.stride(-1) != 1:
-        raise ValueError("the head dimension must be contiguous")
-    return [d if n == 1 else st for n, st in zip(t.shape[:-1], t.stride()[:-1])]
-
-
-def _cache_desc(k, v):
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or not k.is_cuda:
-        raise ValueError("expected two CUDA caches of one type and shape [pages, H_kv, page_size, d]")
-    st = _strides(k)
-    if st != _strides(v):
-        raise ValueError("the caches of K and V must have the same strides")
-    pages, heads, page_size, d = k.shape
-    return KVCacheDesc(k.data_ptr(), v.data_ptr(), _dtype_code(k), pages, page_size, heads, d, *st)
-
-
-def _rows_desc(t, like, heads=None):
-    """Packed rows [T, H, d] of the cache's type."""
-    if t.dim() != 3 or t.dtype != like.dtype or t.device != like.device or t.shape[2] != like.shape[3]:
-        raise ValueError("expected packed rows [T, H, d] of the cache's type, device and head dimension")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"expected {heads} heads, got {t.shape[1]}")
-    return RowsDesc(t.data_ptr(), *_strides(t))
-
-
-def fa_cache_plan(ctx_len, cu_new, block_table, n_pages, free_list, free_count, seq_len, slot, position, page_size: int,
-                  max_new: int, parent=None, tree_mask=None, stream=None) -> None:
-    """Pages, slot map, positions and (with ``parent``) tree masks of a step from the
-    requests' lengths, on the GPU. int32 tensors: ``ctx_len``, ``n_pages``, ``seq_len`` [B],
-    ``cu_new`` [B+1], ``block_table`` [B, max_pages], ``free_list`` [num_pages],
-    ``free_count`` [1], ``slot``, ``position``, ``parent`` [rows]; ``tree_mask`` int64
-    [rows, ceil(max_new/64)]. See include/fa.h for what is read, written and refused."""
-    import torch
-    dev = ctx_len.device
-    if not ctx_len.is_cuda or block_table.dim() != 2:
-        raise ValueError("expected CUDA tensors and a two-dimensional block table")
-    B, rows = ctx_len.numel(), slot.numel()
-    if (cu_new.numel() != B + 1 or block_table.shape[0] != B or n_pages.numel() != B or seq_len.numel() != B
-            or position.numel() != rows or free_count.numel() != 1):
-        raise ValueError("lengths do not fit: cu_new [B+1]; block_table, n_pages, seq_len [B]; position [rows]")
-    a = _ints(dev, torch.int32, ctx_len=ctx_len, cu_new=cu_new)
-    c = _ints(dev, torch.int32, block_table=block_table, n_pages=n_pages, free_list=free_list, free_count=free_count,
-              seq_len=seq_len, slot=slot, position=position)
-    up = words = None
-    if (parent is None) != (tree_mask is None):
-        raise ValueError("parent and tree_mask go together")
-    if parent is not None:
-        if parent.numel() != rows or tuple(tree_mask.shape) != (rows, -(-max_new // 64)):
-            raise ValueError("expected parent [rows] and tree_mask [rows, ceil(max_new/64)]")
-        up, = _ints(dev, torch.int32, parent=parent)
-        words, = _ints(dev, torch.int64, tree_mask=tree_mask)
-    _call("fa_cache_plan", dev, stream, B, rows, max_new, page_size, free_list.numel(), block_table.shape[1], *a, up, *c,
-          words)
-
-
-def _rope_tables_ptr(dev, positions, inv_freq, axis):
-    import torch
-    if positions.dtype != torch.int32 or positions.device != dev or (positions.shape[-1] > 1
-                                                                     and positions.stride(-1) != 1):
-        raise ValueError("positions: expected int32 on the same device, contiguous along the tokens")
-    if inv_freq.numel() != axis.numel():
-        raise ValueError("inv_freq and axis hold one entry for each rotated pair")
-    f, = _ints(dev, torch.float32, inv_freq=inv_freq)
-    a, = _ints(dev, torch.uint8, axis=axis)
-    return f, a, 2 * inv_freq.numel()
-
-
-def fa_rope(x, out, positions, inv_freq, axis, inverse: bool = False, pairs: bool = False, stream=None) -> None:
-    """Rotary positions over several axes: ``x`` [B, H, N, d] -> ``out`` (``x`` itself is
-    fine). ``positions`` int32 [axes, B, N] or [axes, N]; ``inv_freq`` fp32 and ``axis`` uint8,
-    one entry for each rotated pair (:func:`rope_tables`). ``inverse`` turns back, which is
-    the gradient. Strided views are taken as they are."""
-    B, H, N, d = _shape(x)
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or not x.is_cuda:
-        raise ValueError("x and out must be CUDA tensors of one shape and type")
-    if positions.dim() == 2:
-        positions = positions[:, None]
-    if positions.dim() != 3 or positions.shape[1] not in (1, B) or positions.shape[2] != N:
-        raise ValueError("expected positions [axes, B, N] or [axes, N]")
-    f, a, rot = _rope_tables_ptr(x.device, positions, inv_freq, axis)
-    three = ctypes.c_longlong * 3
-    _call("fa_rope", x.device, stream, _dtype_code(x), x.data_ptr(), out.data_ptr(), B, H, N, d, three(*_strides(x)),
-          three(*_strides(out)), positions.data_ptr(), positions.stride(0),
-          positions.stride(1) if positions.shape[1] == B else 0, positions.shape[0], f, a, rot, int(bool(inverse)),
-          int(bool(pairs)))
-
-
-def fa_rope_append(q, k, v, q_out, cache_k, cache_v, slot, positions=None, inv_freq=None, axis=None,
-                   pairs: bool = False, stream=None) -> None:
-    """A step's new rows: ``q`` [T, Hq, d] rotated into ``q_out``, ``k`` [T, H_kv, d] rotated and
-    ``v`` as it is written to rows ``slot`` [T] of the caches [pages, H_kv, page_size, d].
-    ``positions`` int32 [axes, T]; without it nothing is rotated. ``q`` and ``q_out`` may be None."""
-    import torch
-    desc = _cache_desc(cache_k, cache_v)
-    T, H_kv, dev = k.shape[0], cache_k.shape[1], cache_k.device
-    rk, rv = _rows_desc(k, cache_k, H_kv), _rows_desc(v, cache_k, H_kv)
-    if v.shape[0] != T or slot.numel() != T or (q is None) != (q_out is None):
-        raise ValueError("k, v and slot hold the same rows; q and q_out go together")
-    rq = ro = None
-    if q is not None:
-        if q.shape != q_out.shape or q.shape[0] != T:
-            raise ValueError("q and q_out hold the same rows as k")
-        rq, ro = _rows_desc(q, cache_k), _rows_desc(q_out, cache_k)
-        rq, ro, heads = ctypes.byref(rq), ctypes.byref(ro), q.shape[1]
-    else:
-        heads = 0
-    s, = _ints(dev, torch.int32, slot=slot)
-    p = f = a = None
-    rot = axes = stride = 0
-    if positions is not None:
-        if positions.dim() != 2 or positions.shape[1] != T:
-            raise ValueError("expected positions [axes, T]")
-        f, a, rot = _rope_tables_ptr(dev, positions, inv_freq, axis)
-        p, stride, axes = positions.data_ptr(), positions.stride(0), positions.shape[0]
-    _call("fa_rope_append", dev, stream, ctypes.byref(desc), T, heads, rq, ctypes.byref(rk), ctypes.byref(rv), ro, s, p,
-          stride, axes, f, a, rot, int(bool(pairs)))
-
-
-def fa_tree_fwd_workspace_size(B: int, rows: int, max_q: int, Hq: int, H_kv: int, d: int) -> int:
-    return int(load_library().fa_tree_fwd_workspace_size(B, rows, max_q, Hq, H_kv, d))
-
-
-def fa_tree_fwd(q, cache_k, cache_v, block_table, seq_len, cu_q, o, lse, workspace, max_q: int, tree_mask=None,
-                scale: float | None = None, stream=None) -> None:
-    """Attention of packed rows ``q`` [T, Hq, d] (request b's are ``cu_q[b]`` .. ``cu_q[b+1]-1``,
-    at most ``max_q``) over the first ``seq_len[b]`` rows of its pages; writes ``o`` and ``lse``
-    [T, Hq]. ``tree_mask`` int64 [T, ceil(max_q/64)] as :func:`fa_cache_plan` builds it; None
-    is a chain (decoding, prompt chunks). See include/fa.h."""
-    import torch
-    desc = _cache_desc(cache_k, cache_v)
-    T, Hq, d = q.shape
-    dev, B = cache_k.device, seq_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or cu_q.numel() != B + 1:
-        raise ValueError("expected block_table [B, max_pages], seq_len [B], cu_q [B+1]")
-    rq, ro = _rows_desc(q, cache_k), _rows_desc(o, cache_k, Hq)
-    if o.shape[0] != T or tuple(lse.shape) != (T, Hq) or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("expected o like q, lse [T, Hq] and a contiguous workspace on the same device")
-    if workspace.numel() * workspace.element_size() < fa_tree_fwd_workspace_size(B, T, max_q, Hq, cache_k.shape[1], d):
-        raise ValueError("workspace is smaller than fa_tree_fwd_workspace_size")
-    table, lens, cu = _ints(dev, torch.int32, block_table=block_table, seq_len=seq_len, cu_q=cu_q)
-    out, = _ints(dev, torch.float32, lse=lse)
-    words = None
-    if tree_mask is not None:
-        if tuple(tree_mask.shape) != (T, -(-max_q // 64)):
-            raise ValueError("expected tree_mask [T, ceil(max_q/64)]")
-        words, = _ints(dev, torch.int64, tree_mask=tree_mask)
-    _call("fa_tree_fwd", dev, stream, ctypes.byref(desc), ctypes.byref(rq), ctypes.byref(ro), out, B, T, max_q, Hq,
-          block_table.shape[1], table, cu, lens, words, _scale(scale, d), workspace.data_ptr())
-
-
-def fa_cache_commit(cache_k, cache_v, block_table, ctx_len, accepted, n_accepted, new_len, stream=None) -> None:
-    """Move the accepted path of each request's draft to the front of its new rows:
-    ``accepted`` int32 [B, max_accept] request-local indices, strictly increasing, the first
-    ``n_accepted[b]`` of them; ``new_len[b]`` (may be ``ctx_len``) = rows then kept."""
-    import torch
-    desc = _cache_desc(cache_k, cache_v)
-    B, dev = ctx_len.numel(), cache_k.device
-    if (block_table.dim() != 2 or accepted.dim() != 2 or block_table.shape[0] != B or accepted.shape[0] != B
-            or n_accepted.numel() != B or new_len.numel() != B):
-        raise ValueError("expected block_table [B, max_pages], accepted [B, max_accept], n_accepted and new_len [B]")
-    a = _ints(dev, torch.int32, block_table=block_table, ctx_len=ctx_len, accepted=accepted, n_accepted=n_accepted,
-              new_len=new_len)
-    _call("fa_cache_commit", dev, stream, ctypes.byref(desc), B, block_table.shape[1], accepted.shape[1], *a)
 
 
 def attention_forward(q, k, v, causal: bool = False, block_mask=None, scale=None, stream=None):

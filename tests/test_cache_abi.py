@@ -125,13 +125,17 @@ def test_commit_refusals(lib):
 
 def test_binding_refuses_mismatched_tensors():
     import torch
+
+    from io_aware_exact_19_b200 import paged
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
-        fa._cache_desc(k, k)  # not on a GPU
+        paged._cache_desc(k, k)  # not on a GPU
     with pytest.raises(ValueError):
-        fa._strides(k.transpose(2, 3))
+        paged._strides(k.transpose(2, 3))
     with pytest.raises(ValueError):
-        fa._rows_desc(torch.zeros((3, 2, 32), dtype=torch.bfloat16), k)
+        paged._rows_desc(torch.zeros((3, 2, 32), dtype=torch.bfloat16), k, 2, 3)
     with pytest.raises(ValueError):
-        fa._ints(k.device, torch.int32, slot=torch.zeros(4, dtype=torch.int64))
-    assert fa._strides(torch.zeros((1, 2, 16, 64))) == [64, 1024, 64]
+        paged._addresses(0, torch.int32, torch.zeros(4, dtype=torch.int32))
+    assert paged._strides(torch.zeros((1, 2, 16, 64))) == (64, 1024, 64)
+    with pytest.raises(AttributeError):
+        fa.fa_no_such_call
