@@ -12,200 +12,207 @@ namespace {
 
 // ------------------------------------------------------------------ plan
 //
-// One cluster of 8 CTAs, so that the two places where all requests meet (pages given
-// back before any is taken, tables written before slots are read) are cluster barriers
-// and the whole plan is one launch. It is latency bound: the floor is a launch and a
-// handful of dependent loads. Every CTA reads all lengths and scans the needs itself
-// (a few loads a thread), which is cheaper than handing prefix sums around.
+// Latency bound: the floor is a launch and the loads that wait for one another (lengths, free
+// pages, table). The pages are handed out by one cluster of 8 CTAs, so that the two places where
+// all requests meet (pages given back before any is taken, tables written before slots are read)
+// are cluster barriers and the whole plan is one launch. Every CTA reads all lengths and scans
+// the needs itself, one load's latency, which is cheaper than handing prefix sums around; pages
+// are then given out a thread per page and slots a thread per row.
 //
-// Tree masks: the set of a token's ancestors by pointer doubling. With A_t the mask
-// known so far and up_t the first token not in it, A_t |= A_{up_t}, up_t = up_{up_t}
-// doubles the covered path each round, so ceil(log2(max_new)) rounds suffice; the
-// depth is the number of bits minus one. One thread per token, groups of threads
-// (a power of two >= max_new) per request.
+// Tree masks need no pages: further clusters build them at the same time. The set of a token's
+// ancestors by pointer doubling: with A_t the mask known so far and up_t the first token not in
+// it, A_t |= A_{up_t}, up_t = up_{up_t} doubles the covered path each round, so
+// ceil(log2(max_new)) rounds suffice; the depth is the number of bits minus one. One thread per
+// token, groups of threads (a power of two >= max_new) per request.
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanCtas = 8;
 constexpr int kPlanPer = kCacheMaxB / kPlanThreads;  // requests scanned by a thread
+constexpr int kPlanRows = 4;                         // rows a thread has in flight
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Exclusive prefix sum of x over the CTA; `total` gets the sum. `warp_sums` holds a word per warp.
-__device__ __forceinline__ int scan_exclusive(int x, int* warp_sums, int& total) {
+// Exclusive prefix sums of x and y over the CTA; `all_x`, `all_y` get the sums. `sums` holds two
+// words per warp.
+__device__ __forceinline__ void scan_exclusive(int& x, int& y, int* sums, int& all_x, int& all_y) {
+  constexpr int kWarps = kPlanThreads / 32;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  int s = x;
+  int s = x, t = y;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, k);
-    if (lane >= k) s += y;
+    const int u = __shfl_up_sync(0xffffffffu, s, k), v = __shfl_up_sync(0xffffffffu, t, k);
+    if (lane >= k) {
+      s += u;
+      t += v;
+    }
+  }
+  if (lane == 31) {
+    sums[warp] = s;
+    sums[kWarps + warp] = t;
   }
   __syncthreads();
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  const int w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
-  int before = 0, all = 0;
+  all_x = all_y = 0;
+  int before_x = 0, before_y = 0;
 #pragma unroll
-  for (int i = 0; i < kPlanThreads / 32; ++i) {
-    const int v = __shfl_sync(0xffffffffu, w, i);
-    before += i < warp ? v : 0;
-    all += v;
+  for (int i = 0; i < kWarps; ++i) {
+    const int u = sums[i], v = sums[kWarps + i];
+    before_x += i < warp ? u : 0;
+    before_y += i < warp ? v : 0;
+    all_x += u;
+    all_y += v;
   }
-  total = all;
-  return before + s - x;
+  x = before_x + s - x;
+  y = before_y + t - y;
 }
 
-// What the lengths say of request b, before anything is written.
-struct Wish {
-  int ctx, n, held, want;  // want < 0: takes no part
-};
-
-__device__ __forceinline__ Wish wish_of(const PlanArgs& p, int b) {
-  Wish w;
-  w.ctx = p.ctx_len[b];
-  const long long n = static_cast<long long>(p.cu_new[b + 1]) - p.cu_new[b];
-  w.held = min(max(p.n_pages[b], 0), p.max_pages);
-  const long long want =
-      (static_cast<long long>(w.ctx) + n + (1 << p.page_shift) - 1) >> p.page_shift;
-  const bool ok = w.ctx >= 0 && n >= 0 && n <= p.max_new && want <= p.max_pages;
-  w.n = ok ? static_cast<int>(n) : 0;
-  w.want = ok ? static_cast<int>(want) : -1;
-  return w;
+// The last b of [0, B) with first[b] <= x (first[0] <= x; `first` does not fall).
+__device__ __forceinline__ int find_last(const int* first, int B, int x) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    fa_cache_plan_kernel(const PlanArgs p) {
-  extern __shared__ int plan_smem[];
-  __shared__ int warp_sums[32];
-  int* s_cu = plan_smem;                  // [B + 1]
-  int* s_need = s_cu + p.B + 1;           // [B] pages taken by the requests before b
-  int* s_give = s_need + p.B;             // [B] pages given back before b
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int rank = blockIdx.x;
-  constexpr int kWarps = kPlanThreads / 32;
+// Pages, state, slots (and positions, without trees) by the first cluster.
+__device__ __forceinline__ void plan_pages(const PlanArgs& p, int* smem) {
+  __shared__ int sums[2 * kPlanThreads / 32];
+  int* s_cu = smem;               // [B + 1]
+  int* s_need = s_cu + p.B + 1;   // [B] pages taken by the requests before b
+  int* s_give = s_need + p.B;     // [B] pages given back before b
+  int* s_held = s_give + p.B;     // [B]
+  int* s_want = s_held + p.B;     // [B] -1: takes no part
+  int* s_ctx = s_want + p.B;      // [B]
+  const int tid = threadIdx.x, rank = blockIdx.x;
+  constexpr int kAll = kPlanCtas * kPlanThreads;
+  const int me = rank * kPlanThreads + tid;
   const int free0 = min(max(*p.free_count, 0), p.num_pages);
 
   // Thread t scans requests t * per .. t * per + per - 1.
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
-  int need_mine = 0, give_mine = 0;
-  int need_b[kPlanPer], give_b[kPlanPer];
+  int need = 0, give = 0;
 #pragma unroll
   for (int k = 0; k < kPlanPer; ++k) {
-    need_b[k] = give_b[k] = 0;
     const int b = tid * per + k;
     if (k < per && b < p.B) {
-      const Wish w = wish_of(p, b);
-      if (w.want >= 0) {
-        need_b[k] = max(w.want - w.held, 0);
-        give_b[k] = max(w.held - w.want, 0);
-      }
-      s_cu[b] = p.cu_new[b];
-      need_mine += need_b[k];
-      give_mine += give_b[k];
+      const int ctx = p.ctx_len[b], cu = p.cu_new[b];
+      const long long n = static_cast<long long>(p.cu_new[b + 1]) - cu;
+      const int held = min(max(p.n_pages[b], 0), p.max_pages);
+      const long long pages = (static_cast<long long>(ctx) + n + (1 << p.page_shift) - 1) >> p.page_shift;
+      const bool ok = ctx >= 0 && n >= 0 && n <= p.max_new && pages <= p.max_pages;
+      const int want = ok ? static_cast<int>(pages) : -1;
+      s_cu[b] = cu;
+      s_ctx[b] = ctx;
+      s_held[b] = held;
+      s_want[b] = want;
+      s_need[b] = ok ? max(want - held, 0) : 0;
+      s_give[b] = ok ? max(held - want, 0) : 0;
+      need += s_need[b];
+      give += s_give[b];
     }
   }
   if (tid == 0) s_cu[p.B] = p.cu_new[p.B];
   int need_all, give_all;
-  int need_at = scan_exclusive(need_mine, warp_sums, need_all);
-  int give_at = scan_exclusive(give_mine, warp_sums, give_all);
+  scan_exclusive(need, give, sums, need_all, give_all);
 #pragma unroll
   for (int k = 0; k < kPlanPer; ++k) {
     const int b = tid * per + k;
     if (k < per && b < p.B) {
-      s_need[b] = need_at;
-      s_give[b] = give_at;
-      need_at += need_b[k];
-      give_at += give_b[k];
+      const int x = s_need[b], y = s_give[b];
+      s_need[b] = need;
+      s_give[b] = give;
+      need += x;
+      give += y;
     }
   }
   __syncthreads();
+  auto need_upto = [&](int b) { return b + 1 < p.B ? s_need[b + 1] : need_all; };  // by requests 0 .. b
   const int free1 = min(free0 + give_all, p.num_pages);
 
-  // Pages given back, a warp per request. (give_all is the same in all CTAs.)
+  // Pages given back, then (behind them) pages taken, a thread per page. give_all is the same in
+  // all CTAs of the cluster, so they agree on the barrier.
   if (give_all > 0) {
-    for (int b = rank * kWarps + warp; b < p.B; b += kPlanCtas * kWarps) {
-      const Wish w = wish_of(p, b);
-      if (w.want < 0 || w.held <= w.want) continue;
-      int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-      for (int i = w.want + lane; i < w.held; i += 32) {
-        const int at = free0 + s_give[b] + (i - w.want);
-        if (at < p.num_pages) p.free_list[at] = row[i];
-        row[i] = -1;
+    for (int k = me; k < give_all; k += kAll) {
+      const int b = find_last(s_give, p.B, k);
+      int32_t* entry = p.block_table + static_cast<size_t>(b) * p.max_pages + s_want[b] + (k - s_give[b]);
+      if (free0 + k < p.num_pages) p.free_list[free0 + k] = *entry;
+      *entry = -1;
+    }
+    cluster_barrier();
+  }
+  for (int k = me; k < min(need_all, free1); k += kAll) {
+    const int b = find_last(s_need, p.B, k);
+    if (need_upto(b) <= free1)
+      p.block_table[static_cast<size_t>(b) * p.max_pages + s_held[b] + (k - s_need[b])] = p.free_list[free1 - 1 - k];
+  }
+  cluster_barrier();  // the tables are written, and every CTA has read the state
+
+  auto granted = [&](int b) { return s_want[b] >= 0 && (s_want[b] <= s_held[b] || need_upto(b) <= free1); };
+  for (int b = me; b < p.B; b += kAll) {
+    const bool yes = granted(b);
+    if (yes) p.n_pages[b] = s_want[b];
+    p.seq_len[b] = yes ? s_ctx[b] + (s_cu[b + 1] - s_cu[b]) : 0;
+  }
+  if (me == 0) {
+    // The needs' sums grow, so the granted ones are the first of them.
+    int b = p.B - 1;
+    while (b >= 0 && need_upto(b) > free1) --b;
+    *p.free_count = free1 - (b >= 0 ? need_upto(b) : 0);
+  }
+
+  // Slots, a thread per row, a few rows at a time.
+  const int page_mask = (1 << p.page_shift) - 1;
+  for (int t0 = me; t0 < p.rows; t0 += kPlanRows * kAll) {
+    int at[kPlanRows], page[kPlanRows];
+    bool inside[kPlanRows], few[kPlanRows];
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) {
+      const int t = t0 + k * kAll;
+      at[k] = 0;
+      page[k] = -1;
+      inside[k] = few[k] = false;
+      if (t < p.rows) {
+        const int b = find_last(s_cu, p.B, t);
+        const int i = t - s_cu[b], n = s_cu[b + 1] - s_cu[b];
+        inside[k] = i >= 0 && i < n;
+        few[k] = n <= p.max_new;
+        at[k] = inside[k] ? s_ctx[b] + i : 0;
+        if (inside[k] && granted(b)) page[k] = p.block_table[static_cast<size_t>(b) * p.max_pages + (at[k] >> p.page_shift)];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) {
+      const int t = t0 + k * kAll;
+      if (t < p.rows) {
+        const bool there = page[k] >= 0 && page[k] < p.num_pages;
+        p.slot[t] = there ? (page[k] << p.page_shift) + (at[k] & page_mask) : -1;
+        if (p.parent == nullptr || !inside[k] || !few[k]) p.position[t] = at[k];
       }
     }
   }
-  cluster_barrier();  // every CTA has read the state; the pages given back are in the list
+}
 
-  // Pages taken and the new state, a warp per request.
-  for (int b = rank * kWarps + warp; b < p.B; b += kPlanCtas * kWarps) {
-    const Wish w = wish_of(p, b);
-    const int need = w.want < 0 ? 0 : max(w.want - w.held, 0);
-    const bool granted = w.want >= 0 && (need == 0 || static_cast<long long>(s_need[b]) + need <= free1);
-    if (granted) {
-      int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-      for (int i = lane; i < need; i += 32) row[w.held + i] = p.free_list[free1 - 1 - (s_need[b] + i)];
-    }
-    __syncwarp();
-    if (lane == 0) {
-      if (granted) p.n_pages[b] = w.want;
-      p.seq_len[b] = granted ? w.ctx + w.n : 0;
-    }
-  }
-  if (rank == 0 && tid == 0) {
-    // The needs are a growing sequence of sums, so the granted ones are its first part.
-    int used = 0;
-    for (int b = p.B - 1; b >= 0; --b) {
-      const int upto = b + 1 < p.B ? s_need[b + 1] : need_all;
-      if (upto <= free1) {
-        used = upto;
-        break;
-      }
-    }
-    *p.free_count = free1 - used;
-  }
-  cluster_barrier();  // tables and seq_len are written
-
-  // Slots (and, without trees, positions), a thread per row.
-  for (int t = rank * kPlanThreads + tid; t < p.rows; t += kPlanCtas * kPlanThreads) {
-    int lo = 0, hi = p.B;  // the last b with cu[b] <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    const int i = t - s_cu[lo];
-    const int n = s_cu[lo + 1] - s_cu[lo];
-    const bool inside = i >= 0 && i < n;
-    const int ctx = p.ctx_len[lo];
-    int slot = -1;
-    if (inside && p.seq_len[lo] > 0) {
-      const int at = ctx + i;
-      const int page = p.block_table[static_cast<size_t>(lo) * p.max_pages + (at >> p.page_shift)];
-      if (page >= 0 && page < p.num_pages)
-        slot = (page << p.page_shift) + (at & ((1 << p.page_shift) - 1));
-    }
-    p.slot[t] = slot;
-    if (p.parent == nullptr || !inside || n > p.max_new) p.position[t] = inside ? ctx + i : 0;
-  }
-  if (p.parent == nullptr) return;
-
-  // Trees.
+// Masks and positions of drafted trees, by the CTAs behind the first cluster.
+__device__ __forceinline__ void plan_trees(const PlanArgs& p, int* smem, int cta, int ctas) {
   int group = 32;
   while (group < p.max_new) group <<= 1;
-  unsigned long long* s_mask = reinterpret_cast<unsigned long long*>(
-      plan_smem + ((3 * p.B + 1 + 1) / 2) * 2);                     // [threads][words]
+  unsigned long long* s_mask = reinterpret_cast<unsigned long long*>(smem);              // [threads][words]
   int* s_up = reinterpret_cast<int*>(s_mask + static_cast<size_t>(kPlanThreads) * p.words);  // [threads]
-  const int groups = kPlanThreads / group;
+  const int tid = threadIdx.x, groups = kPlanThreads / group;
   const int g = tid / group, i = tid % group, base = g * group;
   const int rounds = 32 - __clz(max(p.max_new - 1, 1));
-  for (int b0 = rank * groups; b0 < p.B; b0 += kPlanCtas * groups) {
+  for (int b0 = cta * groups; b0 < p.B; b0 += ctas * groups) {
     const int b = b0 + g;
-    const int start = b < p.B ? s_cu[b] : 0;
-    const int n = b < p.B ? s_cu[b + 1] - start : 0;
-    const bool mine = n <= p.max_new && i < n && start + i >= 0 && start + i < p.rows;
-    int up = -1;
+    const int start = b < p.B ? p.cu_new[b] : 0;
+    const long long n = b < p.B ? static_cast<long long>(p.cu_new[b + 1]) - start : 0;
+    const bool mine = n <= p.max_new && i < n && start >= 0 && start < p.rows - i;
+    int up = -1, ctx = 0;
     if (mine) {
+      ctx = p.ctx_len[b];
       up = p.parent[start + i];
       if (up < 0 || up >= i) up = -1;
     }
@@ -242,9 +249,16 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
           bits += __popcll(m[w]);
         }
       }
-      p.position[start + i] = p.ctx_len[b] + bits - 1;
+      p.position[start + i] = ctx + bits - 1;
     }
   }
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    fa_cache_plan_kernel(const __grid_constant__ PlanArgs p) {
+  extern __shared__ __align__(8) int plan_smem[];
+  if (blockIdx.x < kPlanCtas) plan_pages(p, plan_smem);
+  else plan_trees(p, plan_smem, blockIdx.x - kPlanCtas, gridDim.x - kPlanCtas);
 }
 
 // ------------------------------------------------------------------ commit
@@ -315,13 +329,22 @@ __global__ void __launch_bounds__(kCommitThreads) fa_cache_commit_kernel(const C
 }  // namespace
 
 int launch_cache_plan(const PlanArgs& a, cudaStream_t stream) {
-  size_t bytes = static_cast<size_t>(((3 * a.B + 1 + 1) / 2) * 2) * 4;
-  if (a.parent != nullptr) bytes += static_cast<size_t>(kPlanThreads) * (8 * a.words + 4);
+  size_t bytes = static_cast<size_t>(6 * a.B + 1) * 4;
+  unsigned clusters = 1;
+  if (a.parent != nullptr) {
+    const size_t trees = static_cast<size_t>(kPlanThreads) * (8 * a.words + 4);
+    bytes = bytes > trees ? bytes : trees;
+    int group = 32;
+    while (group < a.max_new) group <<= 1;
+    const int ctas = (a.B + kPlanThreads / group - 1) / (kPlanThreads / group);
+    const int more = (ctas + kPlanCtas - 1) / kPlanCtas;
+    clusters += more < 17 ? more : 17;  // 18 clusters of 8 fill the SMs
+  }
   if (bytes > 48 * 1024) {
-    const cudaError_t e = host::ensure_dynamic_smem(reinterpret_cast<const void*>(fa_cache_plan_kernel), 96 * 1024);
+    const cudaError_t e = host::ensure_dynamic_smem(reinterpret_cast<const void*>(fa_cache_plan_kernel), 100 * 1024);
     if (e != cudaSuccess) return static_cast<int>(e);
   }
-  fa_cache_plan_kernel<<<kPlanCtas, kPlanThreads, bytes, stream>>>(a);
+  fa_cache_plan_kernel<<<clusters * kPlanCtas, kPlanThreads, bytes, stream>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 
