@@ -1,4 +1,4 @@
-"""Build libfa.so in-tree with nvcc for sm_100a.
+"""Build libfa.so in-tree with nvcc for sm_100a, and _paged.so, the binding of its paged cache.
 
 Usage: ``python -m io_aware_exact_19_b200.build`` (or call :func:`build`).
 Objects go to ``io_aware_exact_19_b200/_build``; the library is
@@ -17,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
+BINDING = os.path.join(HERE, "_paged.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_splitkv.cu", "fa_decode.cu", "fa_dropout.cu", "fa_bwd_noalloc.cu",
            "fa_cache_api.cu", "fa_cache.cu", "fa_rope.cu", "fa_tree.cu"]
@@ -72,11 +73,37 @@ def _check_launch_registers(src: str) -> None:
                 raise RuntimeError(f"{mangled}: {regs} registers at launch, the register split needs {want}")
 
 
+def _build_binding() -> None:
+    """Compile the paged cache's Python binding (_paged.so, against this interpreter and torch)."""
+    import sysconfig
+
+    import torch
+    src, root = os.path.join(CSRC, "paged_binding.cpp"), os.path.dirname(torch.__file__)
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "fa.h"), __file__))
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return
+    tmp = BINDING + ".tmp"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-o", tmp, src,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for d in (sysconfig.get_paths()["include"], INCLUDE, os.path.join(root, "include"),
+                         os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"))
+             for x in ("-isystem", d)),
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the compiler failed for paged_binding.cpp:\n{r.stderr[-4000:]}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every CUDA source for sm_100a and link libfa.so; returns its path."""
+    """Compile every CUDA source for sm_100a and link libfa.so, and build the binding of the
+    paged cache next to it; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding.result()
     for src in SOURCES:
         _check_launch_registers(src)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):

@@ -123,19 +123,23 @@ def test_commit_refusals(lib):
     assert commit(B=4097) == UNSUPPORTED
 
 
-def test_binding_refuses_mismatched_tensors():
+def test_binding_refuses_mismatched_tensors(lib):
     import torch
-
-    from io_aware_exact_19_b200 import paged
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        paged._cache_desc(k, k)  # not on a GPU
-    with pytest.raises(ValueError):
-        paged._strides(k.transpose(2, 3))
-    with pytest.raises(ValueError):
-        paged._rows_desc(torch.zeros((3, 2, 32), dtype=torch.bfloat16), k, 2, 3)
-    with pytest.raises(ValueError):
-        paged._addresses(0, torch.int32, torch.zeros(4, dtype=torch.int32))
-    assert paged._strides(torch.zeros((1, 2, 16, 64))) == (64, 1024, 64)
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    lse, ws = torch.zeros(3, 2), torch.zeros(1 << 20, dtype=torch.uint8)
+    # nothing here is on a GPU, and several shapes do not fit: refused before any call
+    for call in (lambda: fa.fa_rope_append(x, x, x, x, k, k, i32(3)),
+                 lambda: fa.fa_rope_append(x, x, x, x, k, k[:3], i32(3)),
+                 lambda: fa.fa_rope_append(x, x, x, x, k[0], k[0], i32(3)),
+                 lambda: fa.fa_tree_fwd(x, k, k, i32(1, 4), i32(1), i32(2), x, lse, ws, max_q=3),
+                 lambda: fa.fa_cache_commit(k, k, i32(1, 4), i32(1), i32(1, 2), i32(1), i32(1)),
+                 lambda: fa.fa_rope(x[None], x[None], i32(1, 2), torch.zeros(32), torch.zeros(32, dtype=torch.uint8)),
+                 lambda: fa.fa_cache_plan(i32(1), i32(2), i32(1, 4), i32(1), i32(4), i32(1), i32(1), i32(1), i32(1), 16, 1)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        fa.fa_cache_commit(None, k, i32(1, 4), i32(1), i32(1, 2), i32(1), i32(1))
     with pytest.raises(AttributeError):
         fa.fa_no_such_call
