@@ -70,6 +70,7 @@ int launch_t(const TreeArgs& a, cudaStream_t stream) {
   p.Hq = a.Hq;
   p.H_kv = a.cache.H_kv;
   p.G = a.Hq / a.cache.H_kv;
+  p.by_group = tree::Divider::of(p.G);
   p.d = a.cache.d;
   p.num_pages = a.cache.num_pages;
   p.max_pages = a.max_pages;

@@ -40,12 +40,27 @@ constexpr float kRescale = 8.0f;
 constexpr uint64_t kDrainNs = 2000000000ull;  // limit of the waits on the abort path
 constexpr float kNoKey = 1e30f;  // minus the reference of a column that has seen no key
 
+// Division of x in [0, 2^31) by a number known at launch: q = (hi32(x * mul) + x) >> shift.
+struct Divider {
+  uint32_t by, mul, shift;
+  static Divider of(int d) {
+    Divider r{static_cast<uint32_t>(d), 0, 0};
+    while ((1ull << r.shift) < r.by) ++r.shift;
+    r.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << r.shift) - r.by)) / r.by + 1);
+    return r;
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), mul) + static_cast<uint32_t>(x)) >> shift);
+  }
+};
+
 struct Params {
   const uint16_t* q;
   uint16_t* o;
   float* lse;
   long long q_row, q_head, o_row, o_head;
   int B, rows, Hq, H_kv, G, d, num_pages, max_pages, page_shift, words;
+  Divider by_group;  // G
   const int32_t* block_table;
   const int32_t* cu_q;
   const int32_t* seq_len;
@@ -95,8 +110,16 @@ struct Item {
   int valid;
 };
 
-// x / y, in 32 bits where they suffice.
+// x / y for x >= 0, y > 0: below 2^22 by a reciprocal (the quotient is then off by at most one),
+// else in 32 bits where they suffice.
 __device__ __forceinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 22) == 0) {
+    const int a = static_cast<int>(x), b = static_cast<int>(y);
+    int q = __float2int_rz(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+    const int rest = a - q * b;
+    q += rest >= b ? 1 : (rest < 0 ? -1 : 0);
+    return q;
+  }
   return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
 }
 
@@ -126,10 +149,13 @@ struct Cursor {
   // Tiles request b counts for; also its rows and keys.
   static __device__ __forceinline__ long long weight(const Params& p, int b, int& q0, int& n, int& len, int& units,
                                                      int& tiles) {
-    q0 = min(max(p.cu_q[b], 0), p.rows);
-    n = max(min(p.cu_q[b + 1], p.rows) - q0, 0);
-    len = static_cast<int>(
-        min(static_cast<long long>(max(p.seq_len[b], 0)), static_cast<long long>(p.max_pages) << p.page_shift));
+    return weight(p, p.cu_q[b], p.cu_q[b + 1], p.seq_len[b], q0, n, len, units, tiles);
+  }
+  static __device__ __forceinline__ long long weight(const Params& p, int cu0, int cu1, int seq, int& q0, int& n, int& len,
+                                                     int& units, int& tiles) {
+    q0 = min(max(cu0, 0), p.rows);
+    n = max(min(cu1, p.rows) - q0, 0);
+    len = static_cast<int>(min(static_cast<long long>(max(seq, 0)), static_cast<long long>(p.max_pages) << p.page_shift));
     units = static_cast<int>((static_cast<long long>(n) * p.G + N - 1) / N);
     tiles = p.by_unit ? 1 : max((len + kKeys - 1) / kKeys, 1);
     return static_cast<long long>(p.H_kv) * units * tiles;
@@ -150,9 +176,9 @@ struct Cursor {
     if (p.tree_mask == nullptr) {
       // The chain's reach: the unit's last token sees keys up to its own. (seq_len may say
       // more than the pages hold; the tokens' places follow seq_len.)
-      const int reach = ctx + min((r0 + N - 1) / p.G, n - 1) + 1;
+      const int reach = ctx + min(p.by_group(r0 + N - 1), n - 1) + 1;
       t1 = min(t1, reach <= 0 ? 0 : (reach - 1) / kKeys + 1);
-      whole_to += r0 / p.G + 1;
+      whole_to += p.by_group(r0) + 1;
     }
     it.ctx = ctx;
     it.b = b;
@@ -228,10 +254,16 @@ struct Smem {
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
-// Reduce v[c] over the 32 lanes for each of C columns: lane l ends with column l (C = 32) or
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sum v[c] over the 32 lanes for each of C columns: lane l ends with column l (C = 32) or
 // l / 2 (C = 16) in v[0].
-template <int C, bool kMax>
-__device__ __forceinline__ void reduce_columns(float (&v)[C]) {
+template <int C>
+__device__ __forceinline__ void sum_columns(float (&v)[C]) {
   const int lane = lane_id();
 #pragma unroll
   for (int o = 16, cnt = C / 2; o > 0; o >>= 1, cnt >>= 1) {
@@ -240,12 +272,10 @@ __device__ __forceinline__ void reduce_columns(float (&v)[C]) {
 #pragma unroll
       for (int i = 0; i < cnt; ++i) {
         const float send = up ? v[i] : v[i + cnt], keep = up ? v[i + cnt] : v[i];
-        const float got = __shfl_xor_sync(0xffffffffu, send, o);
-        v[i] = kMax ? fmaxf(keep, got) : keep + got;
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
       }
     } else {
-      const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
-      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
     }
   }
 }
@@ -286,7 +316,7 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
 template <int D, bool BF16, int N>
 __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                   const Params p) {
+                   const __grid_constant__ Params p) {
   using L = Smem<D, N>;
   constexpr int S = L::kStages, C = L::kCols, kSoftWarps = 4 * L::kGroups;
   constexpr int kThreads = 128 * L::kGroups + 96;
@@ -311,6 +341,9 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
   constexpr uint32_t kTmemO = 256;  // O^T columns; S^T buffers at 0 and N
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // The first requests' lengths, asked for before anything else is set up.
+  const int mine_b = min(tid, p.B - 1);
+  const int cu0 = p.cu_q[mine_b], cu1 = p.cu_q[mine_b + 1], seq = p.seq_len[mine_b];
   if (tid == 0) {
     *abort_flag = 0;
     first_item->valid = 0;
@@ -346,7 +379,9 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
     int q0 = 0, n = 0, len = 0, units = 1, tiles = 1;
     for (int base = 0; base < p.B; base += kThreads) {
       const int b = base + tid;
-      w = b < p.B ? Cursor<N>::weight(p, b, q0, n, len, units, tiles) : 0;
+      if (base == 0) w = Cursor<N>::weight(p, cu0, cu1, seq, q0, n, len, units, tiles);
+      else if (b < p.B) w = Cursor<N>::weight(p, b, q0, n, len, units, tiles);
+      if (b >= p.B) w = 0;
       long long s = w;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
@@ -559,19 +594,29 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
 
     auto load_q = [&](const Item& it) {
       // Query rows r0 .. r0 + N - 1 of the unit, swizzled as TMA would; rows past the last and
-      // columns past d are zero.
-      constexpr int kVecs = N * D / 8;
-      const int rows = it.n * p.G - it.r0;
-#pragma unroll 2
-      for (int v = tid; v < kVecs; v += 128 * L::kGroups) {
-        const int row = v / (D / 8), c = v % (D / 8);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < rows && 8 * c < p.d) {
-          const int tok = (it.r0 + row) / p.G, g = (it.r0 + row) - tok * p.G;
-          x = *reinterpret_cast<const uint4*>(p.q + (it.q0 + tok) * p.q_row + (it.h * p.G + g) * p.q_head + 8 * c);
+      // columns past d are zero. A thread's loads are all asked for before the first is stored.
+      constexpr int kVecs = N * D / 8, kSoft = 128 * L::kGroups, kEach = kVecs / kSoft < 4 ? kVecs / kSoft : 4;
+      static_assert(kVecs % (kSoft * kEach) == 0, "Q's pieces are shared out evenly");
+      const int r0 = it.r0, rows = it.n * p.G - r0;
+      const uint16_t* from = p.q + it.q0 * p.q_row + it.h * p.G * p.q_head;
+#pragma unroll 1
+      for (int v0 = tid; v0 < kVecs; v0 += kSoft * kEach) {
+        uint4 x[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int row = (v0 + k * kSoft) / (D / 8), c = (v0 + k * kSoft) % (D / 8);
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (row < rows && 8 * c < p.d) {
+            const int tok = p.by_group(r0 + row), g = (r0 + row) - tok * p.G;
+            x[k] = *reinterpret_cast<const uint4*>(from + tok * p.q_row + g * p.q_head + 8 * c);
+          }
         }
-        sts128(smem_u32(smem + L::kQOff) + (c / 8) * (N * 128) + row * 128 + ((c % 8) ^ (row % 8)) * 16, x.x, x.y, x.z,
-               x.w);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int row = (v0 + k * kSoft) / (D / 8), c = (v0 + k * kSoft) % (D / 8);
+          sts128(smem_u32(smem + L::kQOff) + (c / 8) * (N * 128) + row * 128 + ((c % 8) ^ (row % 8)) * 16, x[k].x, x[k].y,
+                 x[k].z, x[k].w);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -619,7 +664,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         } else if (own - lane + 31 >= 0) {
           // Lane i fetches the bits of token first + i for the warp's 32 keys; then each key
           // collects its bit of every token.
-          const int first = first_row / p.G, last = min((first_row + C - 1) / p.G, it.n - 1);
+          const int first = p.by_group(first_row), last = min(p.by_group(first_row + C - 1), it.n - 1);
           const long long base = own - lane;  // of the warp's first key; the context's keys are seen
           uint32_t bits = 0;
           if (first + lane <= last) {
@@ -692,8 +737,13 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
           }
 #pragma unroll
           for (int c = 0; c < C; ++c) x[c] = ((seen >> c) & 1u) ? x[c] * sl2 : -INFINITY;
-          reduce_columns<C, true>(x);
-          red[quarter * C + (C == 32 ? lane : lane / 2)] = x[0];
+#pragma unroll
+          for (int c = 0; c < C; ++c) x[c] = warp_max(x[c]);
+          if (lane == 0) {
+#pragma unroll
+            for (int c = 0; c < C; c += 4)
+              *reinterpret_cast<float4*>(red + quarter * C + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+          }
           group_barrier(bar_id);
           if (gt < C) {
             const float high = fmaxf(fmaxf(red[gt], red[C + gt]), fmaxf(red[2 * C + gt], red[3 * C + gt])) - kBias;
@@ -763,11 +813,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
 
       // ---------------------------------------------------------- the run's result
       const bool some = n > n_first;
-      if (some) {
-        wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
-        tc_fence_after();
-      }
-      reduce_columns<C, false>(l);
+      sum_columns<C>(l);
       red[quarter * C + (C == 32 ? lane : lane / 2)] = l[0];
       group_barrier(bar_id);
       const bool whole = it.take == it.tiles;
@@ -781,7 +827,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         ref[gt] = kNoKey;
         if (whole) {
           if (gt < left) {
-            const int rr = it.r0 + col0 + gt, tok = rr / p.G;
+            const int rr = it.r0 + col0 + gt, tok = p.by_group(rr);
             p.lse[static_cast<size_t>(it.q0 + tok) * p.Hq + it.h * p.G + rr - tok * p.G] = lse2 * 0.6931471805599453f;
           }
         } else {
@@ -789,15 +835,24 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         }
       }
       group_barrier(bar_id);
+      if (some) {
+        wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
+        tc_fence_after();
+      }
 #pragma unroll 1
       for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
         const uint32_t t_o = tmem + lanes + kTmemO + half * N + col0;
         // M = 64 keeps row i in lane 32 * (i / 16) + i % 16.
         const int e = D == 64 ? quarter * 16 + lane : half * 128 + r;
         const bool mine = (D != 64 || lane < 16) && e < p.d;
-        int tok = (it.r0 + col0) / p.G, g = (it.r0 + col0) - tok * p.G;
+        const int tok = p.by_group(it.r0 + col0);
+        int g = (it.r0 + col0) - tok * p.G;
+        // The next head of the token, or the next token's first.
+        const long long step = p.o_head, wrap = p.o_row - (p.G - 1) * p.o_head;
+        uint16_t* dst = p.o + (it.q0 + tok) * p.o_row + (it.h * p.G + g) * p.o_head + e;
+        float* part = p.part_o + (static_cast<size_t>(slot) * N + col0) * D + e;
 #pragma unroll 1
-        for (int c = 0; c < C; c += 16) {
+        for (int c = 0; c < C; c += 16, part += 16 * D) {
           uint32_t o[16];
           if (some) {
             tmem_ld16(t_o + c, o);
@@ -806,17 +861,20 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float f = factor[c + i];
-            const float y = some ? (f == 0.0f ? 0.0f : __uint_as_float(o[i]) * f) : 0.0f;
-            if (whole) {
-              if (mine && c + i < left)
-                p.o[(it.q0 + tok) * p.o_row + (it.h * p.G + g) * p.o_head + e] =
-                    static_cast<uint16_t>(pack2<BF16>(y, 0.0f));
-              if (++g == p.G) {
-                g = 0;
-                ++tok;
-              }
-            } else if (mine) {
-              p.part_o[(static_cast<size_t>(slot) * N + col0 + c + i) * D + e] = y;
+            o[i] = some && f != 0.0f ? __float_as_uint(__uint_as_float(o[i]) * f) : 0u;
+          }
+          if (!whole) {
+            if (mine) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) part[i * D] = __uint_as_float(o[i]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (mine && c + i < left) *dst = static_cast<uint16_t>(pack2<BF16>(__uint_as_float(o[i]), 0.0f));
+              const bool next = ++g == p.G;
+              dst += next ? wrap : step;
+              g = next ? 0 : g;
             }
           }
         }
@@ -891,7 +949,7 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const Params p) {
     }
   }
   const float inv = z > 0.0f ? 1.0f / z : z;
-  const int tok = rr / p.G, head = u.x * p.G + rr - tok * p.G;
+  const int tok = p.by_group(rr), head = u.x * p.G + rr - tok * p.G;
   uint16_t* dst = p.o + (a.w + tok) * p.o_row + head * p.o_head + lane * kPer;
 #pragma unroll
   for (int k = 0; k < kPer; k += 2)
