@@ -903,48 +903,65 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
 // Joins the pieces of a cut unit: lse = log sum_s exp(lse_s), O = sum_s exp(lse_s - lse) O_s.
 // Block (w, y): rows 8y .. 8y + 7 of the unit whose first piece worker w holds, a warp a row.
 template <int D, bool BF16, int N>
-__global__ void __launch_bounds__(256) fa_tree_merge_kernel(const Params p) {
+__global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int w = blockIdx.x, lane = threadIdx.x % 32, c = blockIdx.y * 8 + threadIdx.x / 32;
-  const int4 a = p.cuts[2 * w];
+  const int4 a = p.cuts[2 * w], u = p.cuts[2 * w + 1];  // u: cache head, first row, rows of the request
   if (a.x == 0 || c >= N) return;
-  const int4 u = p.cuts[2 * w + 1];  // cache head, first row, rows of the request
   const int rr = u.y + c;
   if (rr >= u.z * p.G) return;
   const int pieces = a.z - w + 1;
-  auto slot_of = [&](int i) { return i == 0 ? a.y : 2 * (w + i); };
-  // Largest piece, then each piece's weight, 32 at a time, a lane each; the rows' loads do not
-  // depend on one another.
-  float m = -INFINITY;
-  bool nan = false;
-  for (int i = lane; i < pieces; i += 32) {
-    const float x = p.part_lse[static_cast<size_t>(slot_of(i)) * N + c];
-    nan |= x != x;
-    m = fmaxf(m, x);
-  }
+  auto row_of = [&](int i) { return static_cast<size_t>(i == 0 ? a.y : 2 * (w + i)) * N + c; };
+  // A lane holds the lse of one piece, of 32 at a time, and kPer consecutive elements of O. The
+  // first pieces' O is asked for together with the lse's, before their weights are known.
+  constexpr int kPer = D / 32, kFirst = 8;
+  float o[kFirst][kPer];
+  auto load_o = [&](int i, float (&to)[kPer]) {
+    const float2* src = reinterpret_cast<const float2*>(p.part_o + row_of(i) * D + lane * kPer);
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    for (int k = 0; k < kPer; k += 2) {
+      const float2 y = src[k / 2];
+      to[k] = y.x;
+      to[k + 1] = y.y;
+    }
+  };
+  float x = lane < pieces ? p.part_lse[row_of(lane)] : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) load_o(min(i, pieces - 1), o[i]);
+  float m = x;
+  bool nan = x != x;
+  for (int i = lane + 32; i < pieces; i += 32) {
+    const float y = p.part_lse[row_of(i)];
+    nan |= y != y;
+    m = fmaxf(m, y);
+  }
+  m = warp_max(m);
   nan = __any_sync(0xffffffffu, nan);
-  constexpr int kPer = D / 32;  // elements of a lane, consecutive
   float z = 0.0f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
+  auto add = [&](float f, const float (&y)[kPer]) {
+    z += f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = fmaf(f, y[k], acc[k]);
+  };
   if (m != -INFINITY || nan) {
     for (int i0 = 0; i0 < pieces; i0 += 32) {
-      const float x = i0 + lane < pieces ? p.part_lse[static_cast<size_t>(slot_of(i0 + lane)) * N + c] : -INFINITY;
+      if (i0 > 0) x = i0 + lane < pieces ? p.part_lse[row_of(i0 + lane)] : -INFINITY;
       const float weight = x == -INFINITY ? 0.0f : ex2(x - m);
       const int here = min(32, pieces - i0);
-#pragma unroll 4
-      for (int i = 0; i < here; ++i) {
-        const float f = __shfl_sync(0xffffffffu, weight, i);
-        z += f;
-        const float* src = p.part_o + (static_cast<size_t>(slot_of(i0 + i)) * N + c) * D + lane * kPer;
+      if (i0 == 0) {
 #pragma unroll
-        for (int k = 0; k < kPer; k += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(src + k);
-          acc[k] = fmaf(f, y.x, acc[k]);
-          acc[k + 1] = fmaf(f, y.y, acc[k + 1]);
+        for (int i = 0; i < kFirst; ++i) {
+          const float f = __shfl_sync(0xffffffffu, weight, i);
+          if (i < here) add(f, o[i]);
         }
+      }
+#pragma unroll 4
+      for (int i = i0 == 0 ? kFirst : 0; i < here; ++i) {
+        float y[kPer];
+        load_o(i0 + i, y);
+        add(__shfl_sync(0xffffffffu, weight, i), y);
       }
     }
   }
