@@ -716,25 +716,34 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
           }
         };
         const bool first = n == n_first;
-        bool move = first;
-        if (!first) {
-          against_ref();
-          float top[4] = {x[0], x[1], x[2], x[3]};
+        if (first) {
+          // The run's first reference of each column: the largest of four of its scores. Any score
+          // within 2^8 of the largest will do, and the vote below catches the rest.
+          if (lane == 0) {
 #pragma unroll
-          for (int c = 4; c < C; c += 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[c + i]);
+            for (int c = 0; c < C; ++c) red[quarter * C + c] = ((seen >> c) & 1u) ? x[c] * sl2 : -INFINITY;
           }
-          move = group_any(bar_id, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kRescale + kBias);
+          group_barrier(bar_id);
+          if (gt < C) {
+            const float high = fmaxf(fmaxf(red[gt], red[C + gt]), fmaxf(red[2 * C + gt], red[3 * C + gt])) - kBias;
+            if (high > -kNoKey) ref[gt] = -high;
+          }
+          group_barrier(bar_id);
         }
-        if (move) {
-          // Some column's reference moves (or is set, by the run's first tile). P V of the tile
-          // before, which adds to O, must be complete.
+        against_ref();
+        float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < C; c += 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[c + i]);
+        }
+        if (group_any(bar_id, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kRescale + kBias)) {
+          // Some column's reference moves. P V of the tile before, which adds to O, must be complete.
           if (!first) {
             wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
             tc_fence_after();
-            load_scores<C>(t_s, x);
           }
+          load_scores<C>(t_s, x);
 #pragma unroll
           for (int c = 0; c < C; ++c) x[c] = ((seen >> c) & 1u) ? x[c] * sl2 : -INFINITY;
 #pragma unroll
@@ -839,17 +848,14 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
         tc_fence_after();
       }
+      constexpr int kOutBytes = D == 64 ? 128 : 256, kOutRows = kOutBytes / 64;
+      uint8_t* stage = smem + L::kPOff + (group / 2) * (kKeys * 128) + (group % 2) * 64;
 #pragma unroll 1
       for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
         const uint32_t t_o = tmem + lanes + kTmemO + half * N + col0;
         // M = 64 keeps row i in lane 32 * (i / 16) + i % 16.
         const int e = D == 64 ? quarter * 16 + lane : half * 128 + r;
         const bool mine = (D != 64 || lane < 16) && e < p.d;
-        const int tok = p.by_group(it.r0 + col0);
-        int g = (it.r0 + col0) - tok * p.G;
-        // The next head of the token, or the next token's first.
-        const long long step = p.o_head, wrap = p.o_row - (p.G - 1) * p.o_head;
-        uint16_t* dst = p.o + (it.q0 + tok) * p.o_row + (it.h * p.G + g) * p.o_head + e;
         float* part = p.part_o + (static_cast<size_t>(slot) * N + col0) * D + e;
 #pragma unroll 1
         for (int c = 0; c < C; c += 16, part += 16 * D) {
@@ -863,20 +869,34 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
             const float f = factor[c + i];
             o[i] = some && f != 0.0f ? __float_as_uint(__uint_as_float(o[i]) * f) : 0u;
           }
+          if (!mine) continue;
           if (!whole) {
-            if (mine) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) part[i * D] = __uint_as_float(o[i]);
-            }
+            for (int i = 0; i < 16; ++i) part[i * D] = __uint_as_float(o[i]);
           } else {
+            // Turned around through the group's part of P, free by now: 64 bytes of each of its
+            // 128 rows, kOutRows of them for a column's kOutBytes.
+            const int at = e % (kOutBytes / 2) * 2;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (mine && c + i < left) *dst = static_cast<uint16_t>(pack2<BF16>(__uint_as_float(o[i]), 0.0f));
-              const bool next = ++g == p.G;
-              dst += next ? wrap : step;
-              g = next ? 0 : g;
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint16_t*>(stage + ((c + i) * kOutRows + at / 64) * 128 + at % 64) =
+                  static_cast<uint16_t>(pack2<BF16>(__uint_as_float(o[i]), 0.0f));
+          }
+        }
+        if (whole) {
+          group_barrier(bar_id);
+          constexpr int kVecs = kOutBytes / 16;
+#pragma unroll 2
+          for (int v = gt; v < C * kVecs; v += 128) {
+            const int c = v / kVecs, at = v % kVecs * 16, rr = it.r0 + col0 + c;
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + (c * kOutRows + at / 64) * 128 + at % 64);
+            const int d0 = half * 128 + at / 2;
+            if (c < left && d0 < p.d) {
+              const int tok = p.by_group(rr), g = rr - tok * p.G;
+              *reinterpret_cast<uint4*>(p.o + (it.q0 + tok) * p.o_row + (it.h * p.G + g) * p.o_head + d0) = y;
             }
           }
+          if (D == 256) group_barrier(bar_id);  // the second half takes the same place
         }
       }
       tc_fence_before();
