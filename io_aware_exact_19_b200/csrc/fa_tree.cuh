@@ -593,31 +593,26 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
     float l[C];
 
     auto load_q = [&](const Item& it) {
-      // Query rows r0 .. r0 + N - 1 of the unit, swizzled as TMA would; rows past the last and
-      // columns past d are zero. A thread's loads are all asked for before the first is stored.
-      constexpr int kVecs = N * D / 8, kSoft = 128 * L::kGroups, kEach = kVecs / kSoft < 4 ? kVecs / kSoft : 4;
-      static_assert(kVecs % (kSoft * kEach) == 0, "Q's pieces are shared out evenly");
+      // Query rows r0 .. r0 + N - 1 of the unit, swizzled as TMA would, copied without passing
+      // through registers; rows past the last and columns past d are zero.
+      constexpr int kVecs = N * D / 8;
       const int r0 = it.r0, rows = it.n * p.G - r0;
       const uint16_t* from = p.q + it.q0 * p.q_row + it.h * p.G * p.q_head;
-#pragma unroll 1
-      for (int v0 = tid; v0 < kVecs; v0 += kSoft * kEach) {
-        uint4 x[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          const int row = (v0 + k * kSoft) / (D / 8), c = (v0 + k * kSoft) % (D / 8);
-          x[k] = make_uint4(0, 0, 0, 0);
-          if (row < rows && 8 * c < p.d) {
-            const int tok = p.by_group(r0 + row), g = (r0 + row) - tok * p.G;
-            x[k] = *reinterpret_cast<const uint4*>(from + tok * p.q_row + g * p.q_head + 8 * c);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          const int row = (v0 + k * kSoft) / (D / 8), c = (v0 + k * kSoft) % (D / 8);
-          sts128(smem_u32(smem + L::kQOff) + (c / 8) * (N * 128) + row * 128 + ((c % 8) ^ (row % 8)) * 16, x[k].x, x[k].y,
-                 x[k].z, x[k].w);
-        }
+      const uint32_t sq = smem_u32(smem + L::kQOff);
+#pragma unroll 2
+      for (int v = tid; v < kVecs; v += 128 * L::kGroups) {
+        const int row = v / (D / 8), c = v % (D / 8);
+        const bool there = row < rows && 8 * c < p.d;
+        const int tok = p.by_group(r0 + row), g = (r0 + row) - tok * p.G;
+        const uint16_t* src = there ? from + tok * p.q_row + g * p.q_head + 8 * c : p.q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + (c / 8) * (N * 128) + row * 128 +
+                                                                           ((c % 8) ^ (row % 8)) * 16),
+                     "l"(src), "r"(there ? 16 : 0)
+                     : "memory");
       }
+    };
+    auto q_loaded = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -636,17 +631,27 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
       walk.unit_at[0] = walk.cur.pos - walk.item[0].take - walk.item[0].t0;
     }
     soft_barrier();
-    if (walk.item[0].valid && walk.item[0].t1 > walk.item[0].t0) load_q(walk.item[0]);
+    if (walk.item[0].valid && walk.item[0].t1 > walk.item[0].t0) {
+      load_q(walk.item[0]);
+      q_loaded();
+    }
     int which = 0, then = 1;
     if (gt == 0 && group == 0 && !p.by_unit) p.cuts[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     while (walk.item[which].valid) {
       const Item& it = walk.item[which];
-      const int t1 = it.t1, len = it.len;
+      const int t1 = it.t1, len = it.len, clean = it.clean;
       if (tid == 0) advance(then);
+      if (p.tree_mask != nullptr && t1 > clean) {
+        // The last tiles' mask words, a token a lane, are near when their turn comes.
+        const int tok = p.by_group(it.r0 + col0) + lane;
+        if (tok < it.n) {
+          const unsigned long long* m = p.tree_mask + static_cast<size_t>(it.q0 + tok) * p.words;
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(m));
+        }
+      }
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] = 0.0f;
       const int n_first = n;
-      const int clean = it.clean;
       for (int t = it.t0; t < t1; ++t, ++n) {
         const int key = t * kKeys + r;
         // Columns that see this thread's key (bit c: column col0 + c).
@@ -818,7 +823,8 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
       }
       // Every S of this unit is read, so Q may be replaced.
       soft_barrier();  // every warp is done with them, and the item that follows is known
-      if (walk.item[then].valid && walk.item[then].t1 > walk.item[then].t0) load_q(walk.item[then]);
+      const bool more = walk.item[then].valid && walk.item[then].t1 > walk.item[then].t0;
+      if (more) load_q(walk.item[then]);  // arrives while the sums are joined
 
       // ---------------------------------------------------------- the run's result
       const bool some = n > n_first;
@@ -843,6 +849,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
           p.part_lse[static_cast<size_t>(slot) * N + col0 + gt] = lse2;
         }
       }
+      if (more) q_loaded();
       group_barrier(bar_id);
       if (some) {
         wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
@@ -872,7 +879,8 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
           if (!mine) continue;
           if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[i * D] = __uint_as_float(o[i]);
+            for (int i = 0; i < 16; ++i)
+              if (c + i < left) part[i * D] = __uint_as_float(o[i]);
           } else {
             // Turned around through the group's part of P, free by now: 64 bytes of each of its
             // 128 rows, kOutRows of them for a column's kOutBytes.
