@@ -34,16 +34,19 @@ EXPORTED = (
     "fa_cache_plan", "fa_rope", "fa_rope_append", "fa_tree_fwd", "fa_tree_fwd_workspace_size", "fa_cache_commit",
 )
 
-# The paged cache's functions live in paged.py, which imports torch; they load on first use.
-_PAGED = ("fa_cache_plan", "fa_rope", "fa_rope_append", "fa_tree_fwd", "fa_tree_fwd_workspace_size", "fa_cache_commit",
-          "KVCacheDesc", "RowsDesc", "TREE_MAX")
+# The paged cache's functions live in paged.py and cache.py, which import torch; they load on first use.
+_PAGED = {"paged": ("fa_cache_plan", "fa_rope", "fa_rope_append", "fa_tree_fwd", "fa_tree_fwd_workspace_size",
+                    "fa_cache_commit", "KVCacheDesc", "RowsDesc", "TREE_MAX"),
+          "cache": ("PagedCache", "Rope", "rope_tables")}
 
 
 def __getattr__(name):
-    if name in _PAGED:
-        from . import paged
-        globals().update({n: getattr(paged, n) for n in _PAGED})
-        return globals()[name]
+    import importlib
+    for module, names in _PAGED.items():
+        if name in names:
+            loaded = importlib.import_module("." + module, __name__)
+            globals().update({n: getattr(loaded, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
@@ -390,10 +393,13 @@ def fa_debug_dropout_draws(B: int, H: int, Nq: int, Nk: int, seed: int, row_majo
     _check(st, "fa_debug_dropout_draws")
 
 
-def attention_forward(q, k, v, causal: bool = False, block_mask=None, scale=None, stream=None):
-    """Allocate O and lse with torch and run the forward; returns (o, lse)."""
+def attention_forward(q, k, v, causal: bool = False, block_mask=None, scale=None, stream=None, rope=None):
+    """Allocate O and lse with torch and run the forward; returns (o, lse). With ``rope`` (a
+    :class:`Rope`) q and k are rotated first."""
     import torch
     B, H, N, d = _shape(q)
+    if rope is not None:
+        q, k = rope.turn(q, stream=stream), rope.turn(k, stream=stream)
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     if block_mask is None:
@@ -404,10 +410,14 @@ def attention_forward(q, k, v, causal: bool = False, block_mask=None, scale=None
 
 
 def attention_backward(q, k, v, o, lse, dout, causal: bool = False, block_mask=None, scale=None,
-                       workspace=None, stream=None):
-    """Allocate dQ, dK, dV (and the workspace if none is given) and run the backward."""
+                       workspace=None, stream=None, rope=None):
+    """Allocate dQ, dK, dV (and the workspace if none is given) and run the backward. With the
+    forward's ``rope``, q and k are those before the rotation (it is done again, not kept) and so
+    are their gradients."""
     import torch
     B, H, N, d = _shape(q)
+    if rope is not None:
+        q, k = rope.turn(q, stream=stream), rope.turn(k, stream=stream)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
         workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), dtype=torch.uint8, device=q.device)
@@ -415,4 +425,7 @@ def attention_backward(q, k, v, o, lse, dout, causal: bool = False, block_mask=N
         fa_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, causal, scale, stream)
     else:
         fa_blocksparse_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, block_mask, causal, scale, stream)
+    if rope is not None:
+        rope.turn(dq, dq, inverse=True, stream=stream)
+        rope.turn(dk, dk, inverse=True, stream=stream)
     return dq, dk, dv
