@@ -356,10 +356,12 @@ fa_status fa_rope_append(const fa_kv_cache* cache, int rows, int Hq, const fa_ro
  * fa_fwd. Rows of no request stay as they were. What the cache holds behind
  * seq_len[b] is never used, whatever it is; K and V of a request's own keys that some
  * row does not see must be finite in V (P = 0 there multiplies them).
- * block_table int32 [B][max_pages], 16-byte aligned q, o. Hq a multiple of H_kv;
- * 1 <= B <= 4096; max_q >= 1, with tree_mask <= FA_TREE_MAX. workspace: DEVICE,
- * 256-byte aligned, fa_tree_fwd_workspace_size() bytes, contents irrelevant; calls
- * that may overlap need one each. scale finite.
+ * block_table int32 [B][max_pages]. Hq a multiple of H_kv; 1 <= B <= 4096; max_q >= 1,
+ * with tree_mask <= FA_TREE_MAX. workspace: DEVICE, 256-byte aligned,
+ * fa_tree_fwd_workspace_size() bytes, contents irrelevant; calls that may overlap need
+ * one each. softmax_scale finite. o must not overlap q. One launch or (units of rows cut
+ * among CTAs, see fa_tree.cuh) two. The results do not depend on the order in which CTAs
+ * run: equal arguments give equal bits.
  */
 size_t fa_tree_fwd_workspace_size(int B, int rows, int max_q, int Hq, int H_kv, int d);
 fa_status fa_tree_fwd(const fa_kv_cache* cache, const fa_rows* q, const fa_rows* o, float* lse, int B, int rows,
@@ -468,6 +470,18 @@ fa_status fa_debug_bwd_withhold(fa_dtype dtype, const void* q, const void* k, co
                                 const float* lse, const void* dout, void* dq, void* dk, void* dv, void* workspace,
                                 int B, int H, int N, int d, float softmax_scale, int causal, int timeout_ms,
                                 cudaStream_t stream);
+
+/*
+ * Debug: fa_tree_fwd with producers that issue no load and every device-side wait
+ * limited to `timeout_ms` (1..5000): the MMA warps' first waits (for K) run out,
+ * record FA_ERR_TIMEOUT and raise the CTA's abort flag; the softmax warps then go
+ * through their remaining steps without waiting, and the CTAs exit. What o and lse
+ * hold for rows with keys is meaningless. Arguments otherwise as fa_tree_fwd.
+ */
+fa_status fa_debug_tree_withhold(const fa_kv_cache* cache, const fa_rows* q, const fa_rows* o, float* lse, int B,
+                                 int rows, int max_q, int Hq, int max_pages, const int32_t* block_table,
+                                 const int32_t* cu_q, const int32_t* seq_len, const uint64_t* tree_mask,
+                                 float softmax_scale, void* workspace, int timeout_ms, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

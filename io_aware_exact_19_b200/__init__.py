@@ -32,6 +32,7 @@ EXPORTED = (
     "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "fa_fwd_splitkv_splits", "fa_debug_bwd_withhold",
     "fa_fwd_dropout", "fa_bwd_dropout", "fa_debug_dropout_draws", "fa_fwd_fp8",
     "fa_cache_plan", "fa_rope", "fa_rope_append", "fa_tree_fwd", "fa_tree_fwd_workspace_size", "fa_cache_commit",
+    "fa_debug_tree_withhold",
 )
 
 # The paged cache's functions live in paged.py and cache.py, which import torch; they load on first use.
@@ -104,6 +105,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fa_tree_fwd_workspace_size": ([i] * 6, sz),
         "fa_tree_fwd": ([vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp, vp, f, vp, vp], i),
         "fa_cache_commit": ([vp, i, i, i, vp, vp, vp, vp, vp, vp], i),
+        "fa_debug_tree_withhold": ([vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp, vp, f, vp, i, vp], i),
     }
     for name, (argtypes, restype) in sigs.items():
         fn = getattr(lib, name)

@@ -74,6 +74,8 @@ struct TreeArgs {
   float scale;
   void* workspace;
   int* status;
+  uint64_t timeout_ns = 2000000000ull;  // limit of every device-side wait
+  int withhold = 0;                     // debug: the producers issue no load
 };
 
 // Limits of the ragged batch and of a drafted tree.

@@ -51,6 +51,49 @@ fa_status check_rope_tables(int n_axes, int rot, int d, const int32_t* positions
 
 fa_status done(int cuda_status) { return cuda_status == 0 ? FA_OK : FA_ERR_CUDA; }
 
+fa_status tree_impl(const fa_kv_cache* cache, const fa_rows* q, const fa_rows* o, float* lse, int B, int rows, int max_q,
+                    int Hq, int max_pages, const int32_t* block_table, const int32_t* cu_q, const int32_t* seq_len,
+                    const uint64_t* tree_mask, float softmax_scale, void* workspace, uint64_t withhold_timeout_ns,
+                    cudaStream_t stream) {
+  fa_status s = check_cache(cache);
+  if (s != FA_OK) return s;
+  s = check_batch(B, rows, max_pages);
+  if (s != FA_OK) return s;
+  if (max_q < 1 || Hq < 1 || Hq % cache->H_kv != 0 || !std::isfinite(softmax_scale)) return FA_ERR_INVALID_ARG;
+  if (Hq > 65535 || (tree_mask != nullptr && max_q > FA_TREE_MAX)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(rows) * Hq > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+  if (rows == 0) return FA_OK;
+  if (!rows_ok(q) || !rows_ok(o) || !aligned(lse, 4)) return FA_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(seq_len, 4)) return FA_ERR_INVALID_ARG;
+  if (tree_mask != nullptr && !aligned(tree_mask, 8)) return FA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return FA_ERR_INVALID_ARG;
+  fa::TreeArgs a{};
+  a.cache = *cache;
+  a.q = *q;
+  a.o = *o;
+  a.lse = lse;
+  a.B = B;
+  a.rows = rows;
+  a.max_q = max_q;
+  a.Hq = Hq;
+  a.max_pages = max_pages;
+  a.page_shift = page_shift_of(cache->page_size);
+  a.words = (max_q + 63) / 64;
+  a.block_table = block_table;
+  a.cu_q = cu_q;
+  a.seq_len = seq_len;
+  a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  a.scale = softmax_scale;
+  a.workspace = workspace;
+  if (withhold_timeout_ns != 0) {
+    a.withhold = 1;
+    a.timeout_ns = withhold_timeout_ns;
+  }
+  a.status = fa::device_status_word();
+  if (a.status == nullptr) return FA_ERR_CUDA;
+  return done(fa::launch_tree_fwd(a, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -203,39 +246,17 @@ fa_status fa_tree_fwd(const fa_kv_cache* cache, const fa_rows* q, const fa_rows*
                       int max_q, int Hq, int max_pages, const int32_t* block_table, const int32_t* cu_q,
                       const int32_t* seq_len, const uint64_t* tree_mask, float softmax_scale, void* workspace,
                       cudaStream_t stream) {
-  fa_status s = check_cache(cache);
-  if (s != FA_OK) return s;
-  s = check_batch(B, rows, max_pages);
-  if (s != FA_OK) return s;
-  if (max_q < 1 || Hq < 1 || Hq % cache->H_kv != 0 || !std::isfinite(softmax_scale)) return FA_ERR_INVALID_ARG;
-  if (Hq > 65535 || (tree_mask != nullptr && max_q > FA_TREE_MAX)) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(rows) * Hq > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
-  if (rows == 0) return FA_OK;
-  if (!rows_ok(q) || !rows_ok(o) || !aligned(lse, 4)) return FA_ERR_INVALID_ARG;
-  if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(seq_len, 4)) return FA_ERR_INVALID_ARG;
-  if (tree_mask != nullptr && !aligned(tree_mask, 8)) return FA_ERR_INVALID_ARG;
-  if (!aligned(workspace, 256)) return FA_ERR_INVALID_ARG;
-  fa::TreeArgs a{};
-  a.cache = *cache;
-  a.q = *q;
-  a.o = *o;
-  a.lse = lse;
-  a.B = B;
-  a.rows = rows;
-  a.max_q = max_q;
-  a.Hq = Hq;
-  a.max_pages = max_pages;
-  a.page_shift = page_shift_of(cache->page_size);
-  a.words = (max_q + 63) / 64;
-  a.block_table = block_table;
-  a.cu_q = cu_q;
-  a.seq_len = seq_len;
-  a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
-  a.scale = softmax_scale;
-  a.workspace = workspace;
-  a.status = fa::device_status_word();
-  if (a.status == nullptr) return FA_ERR_CUDA;
-  return done(fa::launch_tree_fwd(a, stream));
+  return tree_impl(cache, q, o, lse, B, rows, max_q, Hq, max_pages, block_table, cu_q, seq_len, tree_mask, softmax_scale,
+                   workspace, 0, stream);
+}
+
+fa_status fa_debug_tree_withhold(const fa_kv_cache* cache, const fa_rows* q, const fa_rows* o, float* lse, int B,
+                                 int rows, int max_q, int Hq, int max_pages, const int32_t* block_table,
+                                 const int32_t* cu_q, const int32_t* seq_len, const uint64_t* tree_mask,
+                                 float softmax_scale, void* workspace, int timeout_ms, cudaStream_t stream) {
+  if (timeout_ms < 1 || timeout_ms > 5000) return FA_ERR_INVALID_ARG;
+  return tree_impl(cache, q, o, lse, B, rows, max_q, Hq, max_pages, block_table, cu_q, seq_len, tree_mask, softmax_scale,
+                   workspace, static_cast<uint64_t>(timeout_ms) * 1000000ull, stream);
 }
 
 fa_status fa_cache_commit(const fa_kv_cache* cache, int B, int max_pages, int max_accept, const int32_t* block_table,

@@ -88,7 +88,8 @@ int launch_t(const TreeArgs& a, cudaStream_t stream) {
   p.part_lse = reinterpret_cast<float*>(base + ws.part_lse);
   p.cuts = reinterpret_cast<int4*>(base + ws.cuts);
   p.status = a.status;
-  p.timeout_ns = FA_WAIT_TIMEOUT_NS;
+  p.timeout_ns = a.timeout_ns;
+  p.withhold = a.withhold;
 
   auto kern = tree::fa_tree_kernel<D, BF16, N>;
   constexpr int kSmem = tree::Smem<D, N>::kAlloc;

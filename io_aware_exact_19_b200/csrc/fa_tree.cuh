@@ -73,6 +73,7 @@ struct Params {
   int4* cuts;       // [workers][2]: the unit whose first cut piece worker w holds
   int* status;
   uint64_t timeout_ns;
+  int withhold;  // debug: the producers issue no load
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
     bool ok = true;
     Cursor<N> cur = *first_cur;
     Item it = *first_item;
-    for (; ok && it.valid; cur.next(p, it)) {
+    for (; ok && it.valid && !p.withhold; cur.next(p, it)) {
       const int32_t* table = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
       const int head = __shfl_sync(0xffffffffu, it.h, 0);
       // A lane's page of tile t; none (behind the length, or a bad index) is a page past the last,

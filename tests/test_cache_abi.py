@@ -106,6 +106,8 @@ def test_tree_refusals(lib):
     for kw in (dict(B=4097), dict(mask=P, max_q=513), dict(Hq=70000), dict(T=2 ** 30, Hq=4)):
         assert tree(lib, **kw) == UNSUPPORTED, kw
     assert tree(lib, T=0) == fa.FA_OK  # nothing to do
+    assert lib.fa_debug_tree_withhold(ctypes.byref(cache()), ctypes.byref(rows()), ctypes.byref(rows()), P, 2, 4, 8, 4, 3, P,
+                                      P, P, None, 0.125, P, 0, None) == INVALID
     size = lib.fa_tree_fwd_workspace_size
     assert size(2, 4, 8, 4, 2, 64) > 0
     for bad in ((0, 4, 8, 4, 2, 64), (2, -1, 8, 4, 2, 64), (2, 4, 0, 4, 2, 64), (2, 4, 8, 5, 2, 64), (2, 4, 8, 4, 2, 80)):
@@ -143,3 +145,11 @@ def test_binding_refuses_mismatched_tensors(lib):
         fa.fa_cache_commit(None, k, i32(1, 4), i32(1), i32(1, 2), i32(1), i32(1))
     with pytest.raises(AttributeError):
         fa.fa_no_such_call
+
+
+def test_rope_tables(lib):
+    inv, axis = fa.rope_tables(16, [4, 2, 2], device="cpu")
+    assert axis.tolist() == [0, 0, 0, 0, 1, 1, 2, 2] and inv[1].item() == pytest.approx(10000.0 ** -0.125)
+    assert fa.rope_tables(16, [4, 2, 2], interleaved=True, device="cpu")[1].tolist() == [0, 1, 2, 0, 1, 2, 0, 0]
+    with pytest.raises(ValueError):
+        fa.rope_tables(16, [4, 2], device="cpu")

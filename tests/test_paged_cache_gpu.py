@@ -189,11 +189,3 @@ def test_training_with_rotary_positions(B, H, N, d, axes, causal):
     assert max_abs(c.flat(lse), L) <= 2 * 2.0 ** -9 * 6
     DQ, DK, DV = oracle.backward(RQ, RK, V, DO, c.scale, causal=causal)
     assert_grads([(c.flat(g), G) for g, G in zip(grads, (turn(DQ, True), turn(DK, True), DV))])
-
-
-def test_rope_tables():
-    inv, axis = fa.rope_tables(16, [4, 2, 2], device="cpu")
-    assert axis.tolist() == [0, 0, 0, 0, 1, 1, 2, 2] and inv[1].item() == pytest.approx(10000.0 ** -0.125)
-    assert fa.rope_tables(16, [4, 2, 2], interleaved=True, device="cpu")[1].tolist() == [0, 1, 2, 0, 1, 2, 0, 0]
-    with pytest.raises(ValueError):
-        fa.rope_tables(16, [4, 2], device="cpu")

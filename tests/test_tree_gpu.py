@@ -278,3 +278,26 @@ def test_offsets_beyond_32_bits():
     fa.fa_tree_fwd(q, k, v, ints([where]), p.seq_len, p.cu, o2, lse2, workspace(p, 8), max_q=3)
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("d,Hq,max_q", [(64, 2, 2), (128, 8, 20), (256, 4, 40), (128, 8, 200)])
+def test_waits_that_run_out_end_the_call(d, Hq, max_q):
+    # No load is issued, so the waits reach their limit: the call ends, the status tells, and the
+    # next call works.
+    import ctypes
+    p = Paged([700, 5, 0], [max_q, 1, 2], 2, d, 16, "bf16", seed=19)
+    q = queries(p, Hq)
+    want = attend(p, q)
+    o, lse, ws = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"), workspace(p, Hq)
+    desc = fa.KVCacheDesc(p.k.data_ptr(), p.v.data_ptr(), fa.FA_BF16, p.num_pages, 16, 2, d, *p.k.stride()[:3])
+    rows = [fa.RowsDesc(t.data_ptr(), Hq * d, d) for t in (q, o)]
+    st = fa.load_library().fa_debug_tree_withhold(
+        ctypes.byref(desc), *(ctypes.byref(r) for r in rows), lse.data_ptr(), 3, p.T, max_q, Hq, p.table.shape[1],
+        p.table.data_ptr(), p.cu.data_ptr(), p.seq_len.data_ptr(), None, d ** -0.5, ws.data_ptr(), 20,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == fa.FA_OK
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == fa.FA_ERR_TIMEOUT
+    assert fa.fa_device_status() == fa.FA_OK
+    again = attend(p, q)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
