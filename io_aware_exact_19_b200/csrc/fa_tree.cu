@@ -1,5 +1,6 @@
 // Host launcher of the paged tree attention.
 #include "fa_tree.cuh"
+#include "fa_tree_wide.cuh"
 
 #include "fa_cache.h"
 #include "tma_host.h"
@@ -91,11 +92,21 @@ int launch_t(const TreeArgs& a, cudaStream_t stream) {
   p.timeout_ns = a.timeout_ns;
   p.withhold = a.withhold;
 
-  auto kern = tree::fa_tree_kernel<D, BF16, N>;
-  constexpr int kSmem = tree::Smem<D, N>::kAlloc;
+  // More than 64 rows a unit: the kernel with query rows as the MMA's rows.
+  void (*kern)(CUtensorMap, CUtensorMap, tree::Params);
+  int kSmem;
+  unsigned kThreads;
+  if constexpr (N == 128) {
+    kern = tree::fa_tree_wide_kernel<D, BF16>;
+    kSmem = tree::WideSmem<D>::kAlloc;
+    kThreads = 608;
+  } else {
+    kern = tree::fa_tree_kernel<D, BF16, N>;
+    kSmem = tree::Smem<D, N>::kAlloc;
+    kThreads = 128 * tree::Smem<D, N>::kGroups + 96;
+  }
   cudaError_t e = host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  constexpr unsigned kThreads = 128 * tree::Smem<D, N>::kGroups + 96;
   // By unit: request b has at most H_kv * (its rows / N rounded up) units.
   const long long grid = p.by_unit ? static_cast<long long>(p.H_kv) *
                                          ((static_cast<long long>(a.rows) * p.G + N - 1) / N + a.B)

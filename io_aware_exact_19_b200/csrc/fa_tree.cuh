@@ -224,6 +224,37 @@ struct Walk {
   Item item[3];
 };
 
+// Addresses of the barriers: q_full, drain, s_full[2], p_full[2], pv_done[2] (of tile n the one
+// n % 2: a warpgroup may be a tile ahead of another), then k_full, k_empty, v_full, v_empty of
+// each of S stages.
+template <int S>
+struct Bars {
+  static constexpr int kCount = 8 + 4 * S;
+  uint32_t base;
+  __device__ __forceinline__ uint32_t at(int i) const { return base + 8 * i; }
+  __device__ __forceinline__ uint32_t q_full() const { return at(0); }
+  __device__ __forceinline__ uint32_t drain() const { return at(1); }
+  __device__ __forceinline__ uint32_t s_full(int n) const { return at(2 + (n & 1)); }
+  __device__ __forceinline__ uint32_t p_full(int n) const { return at(4 + (n & 1)); }
+  __device__ __forceinline__ uint32_t pv_done(int n) const { return at(6 + (n & 1)); }
+  __device__ __forceinline__ uint32_t k_full(int s) const { return at(8 + s); }
+  __device__ __forceinline__ uint32_t k_empty(int s) const { return at(8 + S + s); }
+  __device__ __forceinline__ uint32_t v_full(int s) const { return at(8 + 2 * S + s); }
+  __device__ __forceinline__ uint32_t v_empty(int s) const { return at(8 + 3 * S + s); }
+};
+
+// What follows the tiles in shared memory, at the same places for both kernels.
+template <int N, int S>
+struct Tail {
+  Walk<N> walk;
+  Cursor<N> first_cur;  // the CTA's first run and where it goes on
+  Item first_item;
+  uint64_t bars[Bars<S>::kCount];
+  int bad_page[2 * S];  // whether a tile has a page index outside the cache
+  uint32_t tmem;
+  int abort_flag;
+};
+
 template <int D, int N>
 struct Smem {
   static constexpr int kCols = N < 32 ? N : 32;            // columns of a softmax thread
@@ -243,15 +274,8 @@ struct Smem {
   static constexpr int kVOff = kKOff + kStages * kTile;
   static constexpr int kRefOff = kVOff + kStages * kTile;  // minus the reference of each column
   static constexpr int kRedOff = kRefOff + 4 * N;          // [group][4 warps][columns]
-  static constexpr int kWalkOff = kRedOff + 4 * 4 * N;
-  static constexpr int kBarOff = (kWalkOff + static_cast<int>(sizeof(Walk<N>)) + 7) / 8 * 8;
-  // q_full, drain, s_full[2], p_full[2], pv_done[2], then k_full, k_empty, v_full, v_empty of each stage
-  static constexpr int kNumBars = 8 + 4 * kStages;
-  static constexpr int kBadOff = kBarOff + 8 * kNumBars;   // [2 * stages] whether a tile has a bad page
-  static constexpr int kMiscOff = (kBadOff + 8 * kStages + 7) / 8 * 8;  // TMEM base, abort flag, first request, its offset
-  static constexpr int kFirstOff = kMiscOff + 16;           // the CTA's first run and where it goes on
-  static constexpr int kBytes = kFirstOff + static_cast<int>(sizeof(Cursor<N>) + sizeof(Item));
-  static constexpr int kAlloc = kBytes;
+  static constexpr int kTailOff = kRedOff + 4 * 4 * N;
+  static constexpr int kAlloc = kTailOff + static_cast<int>(sizeof(Tail<N, kStages>));
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -314,66 +338,52 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
       : "f"(c), "f"(d));
 }
 
-template <int D, bool BF16, int N>
-__global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
-    fa_tree_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                   const __grid_constant__ Params p) {
-  using L = Smem<D, N>;
-  constexpr int S = L::kStages, C = L::kCols, kSoftWarps = 4 * L::kGroups;
-  constexpr int kThreads = 128 * L::kGroups + 96;
-  extern __shared__ __align__(1024) uint8_t smem[];  // the tiles' swizzle counts from 1024-byte boundaries
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  Cursor<N>* first_cur = reinterpret_cast<Cursor<N>*>(smem + L::kFirstOff);
-  Item* first_item = reinterpret_cast<Item*>(smem + L::kFirstOff + sizeof(Cursor<N>));
-  int* bad_page = reinterpret_cast<int*>(smem + L::kBadOff);
-  float* minus_ref = reinterpret_cast<float*>(smem + L::kRefOff);
-  const uint32_t q_full = smem_u32(&bars[0]), drain = smem_u32(&bars[1]);
-  // Of tile n, two of each: with two buffers of P a warpgroup may be a tile ahead of another.
-  auto s_full = [&](int n) { return smem_u32(&bars[2 + (n & 1)]); };
-  auto p_full = [&](int n) { return smem_u32(&bars[4 + (n & 1)]); };
-  auto pv_done = [&](int n) { return smem_u32(&bars[6 + (n & 1)]); };
-  auto k_full = [&](int s) { return smem_u32(&bars[8 + s]); };
-  auto k_empty = [&](int s) { return smem_u32(&bars[8 + S + s]); };
-  auto v_full = [&](int s) { return smem_u32(&bars[8 + 2 * S + s]); };
-  auto v_empty = [&](int s) { return smem_u32(&bars[8 + 3 * S + s]); };
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  constexpr uint32_t kTmemO = 256;  // O^T columns; S^T buffers at 0 and N
+// Where a CTA begins: the first tile of its run, how the tiles are shared out, its TMEM.
+struct Start {
+  long long lo;
+  Share share;
+  uint32_t tmem;
+};
 
+// The start of both kernels: barriers, TMEM, and the CTA's run of tiles. `ring` is shared memory
+// that nothing is loaded into yet (33 KB).
+template <int N, int S, int kThreads, int kSoftWarps>
+__device__ __forceinline__ Start begin(const Params& p, Tail<N, S>& tail, const Bars<S>& bar, uint8_t* ring) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The first requests' lengths, asked for before anything else is set up.
   const int mine_b = min(tid, p.B - 1);
   const int cu0 = p.cu_q[mine_b], cu1 = p.cu_q[mine_b + 1], seq = p.seq_len[mine_b];
   if (tid == 0) {
-    *abort_flag = 0;
-    first_item->valid = 0;
-    first_cur->pos = first_cur->end = 0;
-    mbar_init(q_full, kSoftWarps);
-    mbar_init(drain, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(p_full(i), kSoftWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(pv_done(i), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(s_full(i), 2);  // the commit, and the issuer (for what it has seen)
+    tail.abort_flag = 0;
+    tail.first_item.valid = 0;
+    tail.first_cur.pos = tail.first_cur.end = 0;
+    mbar_init(bar.q_full(), kSoftWarps);
+    mbar_init(bar.drain(), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.s_full(i), 2);  // the commit, and the issuer (for what it has seen)
+      mbar_init(bar.p_full(i), kSoftWarps);
+      mbar_init(bar.pv_done(i), 1);
+    }
     for (int s = 0; s < S; ++s) {
-      mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
+      mbar_init(bar.k_full(s), 1);
+      mbar_init(bar.k_empty(s), 1);
+      mbar_init(bar.v_full(s), 1);
+      mbar_init(bar.v_empty(s), 1);
     }
     fence_barrier_init();
   }
-  for (int c = tid; c < N; c += kThreads) minus_ref[c] = kNoKey;
   if (warp == kSoftWarps + 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(&tail.tmem), 512);
     tmem_relinquish();
   }
 
-  // The CTA's run of tiles: sums of the requests' weights (kept in the ring, which is
-  // still empty); the thread that has the request in which the run begins finds the first item.
   long long lo, total = 0;
   Share share;
+  // The CTA's run of tiles: sums of the requests' weights (kept in the ring, which is
+  // still empty); the thread that has the request in which the run begins finds the first item.
   {
-    long long* before = reinterpret_cast<long long*>(smem + L::kKOff);  // [B]
+    long long* before = reinterpret_cast<long long*>(ring);  // [B]
     long long* warp_sum = before + kCacheMaxB;
     constexpr int kWarps = kThreads / 32;
     long long mine = 0, w = 0;  // of this thread's last request: the weights before it, its own
@@ -406,8 +416,8 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
     if (p.B <= kThreads) {
       if (lo < hi && mine <= lo && lo < mine + w) {
         Cursor<N> c{lo, hi, lo - mine, tid};
-        c.take(p, *first_item, q0, n, len, units, tiles);
-        *first_cur = c;
+        c.take(p, tail.first_item, q0, n, len, units, tiles);
+        tail.first_cur = c;
       }
     } else {
       for (int b = tid; b < p.B && lo < hi; b += kThreads) {
@@ -415,88 +425,157 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         if (from <= lo && lo < to) {
           Cursor<N> c{lo, hi, lo - from, b};
           Cursor<N>::weight(p, b, q0, n, len, units, tiles);
-          c.take(p, *first_item, q0, n, len, units, tiles);
-          *first_cur = c;
+          c.take(p, tail.first_item, q0, n, len, units, tiles);
+          tail.first_cur = c;
         }
       }
     }
   }
   fence_proxy_async_smem();  // TMA writes where the sums were
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // behind every read of the sums
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const WaitCtx ctx{abort_flag, p.status, p.timeout_ns};
-  // (The prefix sums in the ring are not read any more: the barrier above is behind every read.)
+  return {lo, share, tail.tmem};
+}
 
-  if (warp == kSoftWarps || warp == kSoftWarps + 2) {
-    // ------------------------------------------------------------ TMA producers: K, and V
-    // A copy takes about 80 cycles to issue whatever its size, so with small pages (16 rows:
-    // 32 copies a tile) one warp for both would be slower than the memory.
-    const bool is_v = warp != kSoftWarps;
-    const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-    const uint32_t ring = smem_u32(smem) + (is_v ? L::kVOff : L::kKOff);
-    const uint32_t full0 = is_v ? v_full(0) : k_full(0), empty0 = is_v ? v_empty(0) : k_empty(0);
-    const int per_tile = p.page_shift >= 7 ? 1 : kKeys >> p.page_shift;  // pages of a tile
-    const int box_rows = kKeys / per_tile;
-    constexpr int kChunks = D / 64;
-    if (lane == 0) prefetch_tmap(map);
-    int issued = 0, s = 0, ph = 1;
-    bool ok = true;
-    Cursor<N> cur = *first_cur;
-    Item it = *first_item;
-    for (; ok && it.valid && !p.withhold; cur.next(p, it)) {
-      const int32_t* table = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
-      const int head = __shfl_sync(0xffffffffu, it.h, 0);
-      // A lane's page of tile t; none (behind the length, or a bad index) is a page past the last,
-      // which TMA fills with zeros.
-      auto page_of = [&](int t) {
-        const long long key = static_cast<long long>(t) * kKeys + lane * box_rows;
-        return lane < per_tile && key < it.len ? table[key >> p.page_shift] : p.num_pages;
-      };
-      int ahead = it.t0 < it.t1 ? page_of(it.t0) : 0;
-      for (int t = it.t0; t < it.t1; ++t) {
-        int page = ahead;
-        if (t + 1 < it.t1) ahead = page_of(t + 1);
-        const int first_row = per_tile == 1 ? (t * kKeys) & ((1 << p.page_shift) - 1) : 0;
-        bool bad = page < 0 || page >= p.num_pages;
-        if (bad) page = p.num_pages;
-        bad = __any_sync(0xffffffffu, bad && lane < per_tile && static_cast<long long>(t) * kKeys + lane * box_rows < it.len);
-        if (!(ok = mbar_wait_warp(empty0 + 8 * s, ph, ctx))) break;
-        if (lane == 0) {
-          // Twice the stages: the softmax may still look at the tile whose K this one replaces.
-          if (!is_v) bad_page[issued % (2 * S)] = bad;
-          mbar_arrive_expect_tx(full0 + 8 * s, L::kTile);
-        }
-        __syncwarp();
-        // One elected lane issues every page's boxes: their operands are then the same in all lanes.
-        for (int i = 0; i < per_tile; ++i) {
-          const int pg = __shfl_sync(0xffffffffu, page, i);
-          if (elect_one()) {
+// The loading warps, one for K and one for V: every tile of the CTA's runs, in order.
+template <int D, int N, int S>
+__device__ __forceinline__ void load_tiles(const Params& p, Tail<N, S>& tail, const Bars<S>& bar, bool is_v,
+                                           const CUtensorMap* map_k, const CUtensorMap* map_v, uint8_t* k_ring,
+                                           uint8_t* v_ring, const WaitCtx& ctx) {
+  constexpr int kTile = kKeys * D * 2;
+  const int lane = threadIdx.x % 32;
+  // A copy takes about 80 cycles to issue whatever its size, so with small pages (16 rows:
+  // 32 copies a tile) one warp for both would be slower than the memory.
+  const CUtensorMap* map = is_v ? map_v : map_k;
+  const uint32_t ring = smem_u32(is_v ? v_ring : k_ring);
+  const uint32_t full0 = is_v ? bar.v_full(0) : bar.k_full(0), empty0 = is_v ? bar.v_empty(0) : bar.k_empty(0);
+  const int per_tile = p.page_shift >= 7 ? 1 : kKeys >> p.page_shift;  // pages of a tile
+  const int box_rows = kKeys / per_tile;
+  constexpr int kChunks = D / 64;
+  if (lane == 0) prefetch_tmap(map);
+  int issued = 0, s = 0, ph = 1;
+  bool ok = true;
+  Cursor<N> cur = tail.first_cur;
+  Item it = tail.first_item;
+  for (; ok && it.valid && !p.withhold; cur.next(p, it)) {
+    const int32_t* table = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
+    const int head = __shfl_sync(0xffffffffu, it.h, 0);
+    // A lane's page of tile t; none (behind the length, or a bad index) is a page past the last,
+    // which TMA fills with zeros.
+    auto page_of = [&](int t) {
+      const long long key = static_cast<long long>(t) * kKeys + lane * box_rows;
+      return lane < per_tile && key < it.len ? table[key >> p.page_shift] : p.num_pages;
+    };
+    int ahead = it.t0 < it.t1 ? page_of(it.t0) : 0;
+    for (int t = it.t0; t < it.t1; ++t) {
+      int page = ahead;
+      if (t + 1 < it.t1) ahead = page_of(t + 1);
+      const int first_row = per_tile == 1 ? (t * kKeys) & ((1 << p.page_shift) - 1) : 0;
+      bool bad = page < 0 || page >= p.num_pages;
+      if (bad) page = p.num_pages;
+      bad = __any_sync(0xffffffffu, bad && lane < per_tile && static_cast<long long>(t) * kKeys + lane * box_rows < it.len);
+      if (!(ok = mbar_wait_warp(empty0 + 8 * s, ph, ctx))) break;
+      if (lane == 0) {
+        // Twice the stages: the softmax may still look at the tile whose K this one replaces.
+        if (!is_v) tail.bad_page[issued % (2 * S)] = bad;
+        mbar_arrive_expect_tx(full0 + 8 * s, kTile);
+      }
+      __syncwarp();
+      // One elected lane issues every page's boxes: their operands are then the same in all lanes.
+      for (int i = 0; i < per_tile; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, page, i);
+        if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_4d(ring + s * L::kTile + i * box_rows * 128 + c * L::kChunk, map, full0 + 8 * s, c * 64, first_row,
-                          head, pg);
-          }
-        }
-        __syncwarp();
-        ++issued;
-        if (++s == S) {
-          s = 0;
-          ph ^= 1;
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_4d(ring + s * kTile + i * box_rows * 128 + c * kKeys * 128, map, full0 + 8 * s, c * 64, first_row,
+                        head, pg);
         }
       }
+      __syncwarp();
+      ++issued;
+      if (++s == S) {
+        s = 0;
+        ph ^= 1;
+      }
     }
-    if (*abort_flag) {
-      // Aborting: what is in flight lands before the CTA exits; the last load into a stage
-      // completes that stage's phase.
-      for (int i = 0; i < S; ++i)
-        if (issued > i) mbar_wait_bounded(full0 + 8 * i, ((issued - 1 - (issued - 1 - i) % S) / S) & 1, kDrainNs);
+  }
+  if (tail.abort_flag) {
+    // Aborting: what is in flight lands before the CTA exits; the last load into a stage
+    // completes that stage's phase.
+    for (int i = 0; i < S; ++i)
+      if (issued > i) mbar_wait_bounded(full0 + 8 * i, ((issued - 1 - (issued - 1 - i) % S) / S) & 1, kDrainNs);
+  }
+}
+
+// The issuing warp: S of the next tile, then P V of this one. The whole warp walks and waits; one
+// elected lane issues (in issue_s and issue_o), so the operands of each MMA are the same in all
+// lanes and sit in uniform registers.
+template <int N, int S, typename IssueS, typename IssueO>
+__device__ __forceinline__ void issue_tiles(const Params& p, Tail<N, S>& tail, const Bars<S>& bar, const WaitCtx& ctx,
+                                            const IssueS& issue_s, const IssueO& issue_o) {
+  int n = 0, q_count = 0;
+  int s = 0, ph = 0;            // stage and phase of tile n
+  bool ok = true, issued = false;
+  Cursor<N> cur = tail.first_cur;
+  Item it = tail.first_item;
+  for (; ok && it.valid; cur.next(p, it)) {
+    const int tiles = __shfl_sync(0xffffffffu, it.t1 - it.t0, 0);
+    if (tiles == 0) continue;
+    if (!(ok = mbar_wait_warp(bar.q_full(), q_count & 1, ctx))) break;
+    ++q_count;
+    if (!(ok = mbar_wait_warp(bar.k_full(s), ph, ctx))) break;
+    tc_fence_after();
+    issue_s(n, s);
+    issued = true;
+    for (int j = 0; j < tiles; ++j, ++n) {
+      const int s1 = s + 1 == S ? 0 : s + 1, ph1 = s + 1 == S ? ph ^ 1 : ph;
+      if (j + 1 < tiles) {
+        // The other S buffer was read before P of tile n - 1 arrived.
+        if (!(ok = mbar_wait_warp(bar.k_full(s1), ph1, ctx))) break;
+        tc_fence_after();
+        issue_s(n + 1, s1);
+      }
+      if (!(ok = mbar_wait_warp(bar.v_full(s), ph, ctx))) break;
+      if (!(ok = mbar_wait_warp(bar.p_full(n), (n >> 1) & 1, ctx))) break;
+      tc_fence_after();
+      issue_o(n, s, j > 0);
+      s = s1;
+      ph = ph1;
     }
+  }
+  if (!ok && issued) {
+    // Aborting: everything issued completes before TMEM and the operands go.
+    if (elect_one()) {
+      umma_commit(bar.drain());
+      mbar_wait_bounded(bar.drain(), 0, kDrainNs);
+    }
+    __syncwarp();
+  }
+}
+
+template <int D, bool BF16, int N>
+__global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
+    fa_tree_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                   const __grid_constant__ Params p) {
+  using L = Smem<D, N>;
+  constexpr int S = L::kStages, C = L::kCols, kSoftWarps = 4 * L::kGroups;
+  constexpr int kThreads = 128 * L::kGroups + 96;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the tiles' swizzle counts from 1024-byte boundaries
+  Tail<N, S>& tail = *reinterpret_cast<Tail<N, S>*>(smem + L::kTailOff);
+  float* minus_ref = reinterpret_cast<float*>(smem + L::kRefOff);
+  const Bars<S> bar{smem_u32(tail.bars)};
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  constexpr uint32_t kTmemO = 256;  // O^T columns; S^T buffers at 0 and N
+  for (int c = tid; c < N; c += kThreads) minus_ref[c] = kNoKey;
+  const Start start = begin<N, S, kThreads, kSoftWarps>(p, tail, bar, smem + L::kKOff);
+  const uint32_t tmem = start.tmem;
+  const WaitCtx ctx{&tail.abort_flag, p.status, p.timeout_ns};
+
+  if (warp == kSoftWarps || warp == kSoftWarps + 2) {
+    load_tiles<D>(p, tail, bar, warp != kSoftWarps, &tmap_k, &tmap_v, smem + L::kKOff, smem + L::kVOff, ctx);
   } else if (warp == kSoftWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks and waits; one elected lane issues, so the operands of each MMA are
-    // the same in all lanes and sit in uniform registers.
     constexpr uint32_t idesc_s = idesc_f16(BF16, kKeys, N, false, false);
     constexpr int kM = D == 64 ? 64 : 128;
     constexpr uint32_t idesc_o = idesc_f16(BF16, kM, N, true, true);
@@ -514,9 +593,9 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
           umma_ss(tm + (n & 1) * N, sdesc_add(a, (k / 4) * L::kChunk + in), sdesc_add(dQ, (k / 4) * N * 128 + in),
                   idesc_s, k > 0);
         }
-        umma_commit(s_full(n));
-        umma_commit(k_empty(s));
-        mbar_arrive(s_full(n));
+        umma_commit(bar.s_full(n));
+        umma_commit(bar.k_empty(s));
+        mbar_arrive(bar.s_full(n));
       }
       __syncwarp();
     };
@@ -530,49 +609,12 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
           for (int k = 0; k < kKeys / 16; ++k)
             umma_ss(tm + kTmemO + half * N, sdesc_add(a, half * 2 * L::kChunk + k * 2048), sdesc_add(b, k * 2048),
                     idesc_o, k > 0 ? 1u : add);
-        umma_commit(pv_done(n));
-        umma_commit(v_empty(s));
+        umma_commit(bar.pv_done(n));
+        umma_commit(bar.v_empty(s));
       }
       __syncwarp();
     };
-    int n = 0, q_count = 0;
-    int s = 0, ph = 0;            // stage and phase of tile n
-    bool ok = true, issued = false;
-    Cursor<N> cur = *first_cur;
-    Item it = *first_item;
-    for (; ok && it.valid; cur.next(p, it)) {
-      const int tiles = __shfl_sync(0xffffffffu, it.t1 - it.t0, 0);
-      if (tiles == 0) continue;
-      if (!(ok = mbar_wait_warp(q_full, q_count & 1, ctx))) break;
-      ++q_count;
-      if (!(ok = mbar_wait_warp(k_full(s), ph, ctx))) break;
-      tc_fence_after();
-      issue_s(n, s);
-      issued = true;
-      for (int j = 0; j < tiles; ++j, ++n) {
-        const int s1 = s + 1 == S ? 0 : s + 1, ph1 = s + 1 == S ? ph ^ 1 : ph;
-        if (j + 1 < tiles) {
-          // The other S buffer was read before P of tile n - 1 arrived.
-          if (!(ok = mbar_wait_warp(k_full(s1), ph1, ctx))) break;
-          tc_fence_after();
-          issue_s(n + 1, s1);
-        }
-        if (!(ok = mbar_wait_warp(v_full(s), ph, ctx))) break;
-        if (!(ok = mbar_wait_warp(p_full(n), (n >> 1) & 1, ctx))) break;
-        tc_fence_after();
-        issue_o(n, s, j > 0);
-        s = s1;
-        ph = ph1;
-      }
-    }
-    if (!ok && issued) {
-      // Aborting: everything issued completes before TMEM and the operands go.
-      if (elect_one()) {
-        umma_commit(drain);
-        mbar_wait_bounded(drain, 0, kDrainNs);
-      }
-      __syncwarp();
-    }
+    issue_tiles(p, tail, bar, ctx, issue_s, issue_o);
   } else {
     // ------------------------------------------------------------ softmax
     // After a wait ran out every later one returns at once (the abort flag), and the
@@ -616,10 +658,10 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(bar.q_full());
     };
 
-    Walk<N>& walk = *reinterpret_cast<Walk<N>*>(smem + L::kWalkOff);
+    Walk<N>& walk = tail.walk;
     auto soft_barrier = [] { asm volatile("bar.sync 8, %0;" ::"n"(128 * L::kGroups) : "memory"); };
     auto advance = [&](int to) {
       Item& it = walk.item[to];
@@ -627,8 +669,8 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
       walk.unit_at[to] = walk.cur.pos - it.take - it.t0;
     };
     if (tid == 0) {
-      walk.cur = *first_cur;
-      walk.item[0] = *first_item;
+      walk.cur = tail.first_cur;
+      walk.item[0] = tail.first_item;
       walk.unit_at[0] = walk.cur.pos - walk.item[0].take - walk.item[0].t0;
     }
     soft_barrier();
@@ -694,10 +736,10 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
           if (alive) seen = mine;
         }
         }
-        wait_tile(s_full(n), (n >> 1) & 1, ctx);
+        wait_tile(bar.s_full(n), (n >> 1) & 1, ctx);
         tc_fence_after();
         bool masked = t >= clean;
-        if (bad_page[n % (2 * S)]) {
+        if (tail.bad_page[n % (2 * S)]) {
           // A page index outside the cache: its keys are not there.
           masked = true;
           if (key < len) {
@@ -746,7 +788,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         if (group_any(bar_id, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kRescale + kBias)) {
           // Some column's reference moves. P V of the tile before, which adds to O, must be complete.
           if (!first) {
-            wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
+            wait_tile(bar.pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
             tc_fence_after();
           }
           load_scores<C>(t_s, x);
@@ -797,7 +839,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         }
         // P V that read this buffer of P last is complete: with two buffers that of tile n - 2, which
         // was issued before S of this tile, whose commit covers it.
-        if (L::kPBufs == 1 && !first) wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
+        if (L::kPBufs == 1 && !first) wait_tile(bar.pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
         const int buf = n % L::kPBufs;
         const uint32_t p_at = p_row + (N <= 32 ? 0 : buf * L::kPStep);
         const int piece = piece0 + (N <= 32 ? 4 * buf : 0);
@@ -808,7 +850,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         if (t >= clean && t * kKeys + (kKeys - 1) >= len) {
           // The last tile: what the page holds behind the last key may be anything, and 0 * NaN is
           // not 0, so those rows of V are cleared.
-          wait_tile(v_full(n % S), (n / S) & 1, ctx);
+          wait_tile(bar.v_full(n % S), (n / S) & 1, ctx);
           if (key >= len && group == 0) {
             const uint32_t row = smem_u32(smem + L::kVOff + (n % S) * L::kTile) + r * 128;
 #pragma unroll
@@ -820,7 +862,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(n));
+        if (lane == 0) mbar_arrive(bar.p_full(n));
       }
       // Every S of this unit is read, so Q may be replaced.
       soft_barrier();  // every warp is done with them, and the item that follows is known
@@ -834,7 +876,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
       group_barrier(bar_id);
       const bool whole = it.take == it.tiles;
       const long long unit_at = walk.unit_at[which];
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_at > lo ? 1 : 0);
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_at > start.lo ? 1 : 0);
       const int left = it.n * p.G - it.r0 - col0;  // columns of this group that are rows
       if (gt < C) {
         const float sum = (red[gt] + red[C + gt]) + (red[2 * C + gt] + red[3 * C + gt]);
@@ -853,7 +895,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
       if (more) q_loaded();
       group_barrier(bar_id);
       if (some) {
-        wait_tile(pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
+        wait_tile(bar.pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
         tc_fence_after();
       }
       constexpr int kOutBytes = D == 64 ? 128 : 256, kOutRows = kOutBytes / 64;
@@ -911,7 +953,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
       tc_fence_before();
       // The unit that goes on in the next CTAs (at most the last one): what the merge needs to know.
       if (!whole && it.t0 == 0 && gt == 0 && group == 0) {
-        p.cuts[2 * blockIdx.x] = make_int4(1, slot, share.worker(unit_at + it.tiles - 1), it.q0);
+        p.cuts[2 * blockIdx.x] = make_int4(1, slot, start.share.worker(unit_at + it.tiles - 1), it.q0);
         p.cuts[2 * blockIdx.x + 1] = make_int4(it.h, it.r0, it.n, 0);
       }
       group_barrier(bar_id);  // the scratch is read
