@@ -241,7 +241,9 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* v8, float q_sca
  * fa_cache_commit moves the rows of an accepted draft to the front. The batch is
  * ragged and packed: request b owns rows cu[b] .. cu[b+1]-1 of the [rows][heads][d]
  * tensors. All lengths, tables and maps live on the device, so a step can be
- * captured in a CUDA graph and replayed with other lengths.
+ * captured in a CUDA graph and replayed with other lengths (make the first call of
+ * each kind on a device before any capture). Outputs must not overlap inputs, or one
+ * another, except where a comment says so. Offsets into caches and tensors are 64-bit.
  */
 
 /*
@@ -372,7 +374,7 @@ fa_status fa_tree_fwd(const fa_kv_cache* cache, const fa_rows* q, const fa_rows*
 /*
  * Keeps the accepted path of each request's draft: row ctx_len[b] + accepted[b][j] of
  * the cache moves to row ctx_len[b] + j, for j < n_accepted[b], and new_len[b] =
- * ctx_len[b] + the rows kept. accepted int32 [B][max_accept] holds request-local
+ * ctx_len[b] + the rows kept (a request that fa_cache_plan refused accepts none). accepted int32 [B][max_accept] holds request-local
  * indices of new tokens, strictly increasing (a path from the root is); the path ends
  * before the first entry that is not larger than the one before (or is negative), or
  * whose row has no page in the table. new_len may be ctx_len. DEVICE pointers; ctx_len,

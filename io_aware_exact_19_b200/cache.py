@@ -9,8 +9,9 @@ them in the order of a serving step:
         o = cache.attend(layer, q)                  attention               (one or two)
     cache.commit(accepted, count)  or  cache.keep() the rows that stay
 
-Lengths, tables and maps stay on the GPU, so a step can be captured in a CUDA graph (after
-one run outside it) and replayed with other lengths in the same buffers.
+Everything runs on the current stream. Lengths, tables and maps stay on the GPU, so a step can
+be captured in a CUDA graph (after one run outside it) and replayed with other lengths in the
+same buffers.
 """
 from __future__ import annotations
 
@@ -53,7 +54,10 @@ class Rope:
 
     def turn(self, x, out=None, inverse: bool = False, stream=None):
         """``x`` [B, H, N, d] rotated (into a new tensor unless ``out`` is given)."""
-        out = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
+        if out is None:
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            if stream is not None:
+                out.record_stream(stream)
         paged.fa_rope(x, out, self.positions, self.inv_freq, self.axis, inverse=inverse, pairs=self.pairs, stream=stream)
         return out
 
@@ -76,66 +80,68 @@ class PagedCache:
         self.free_count = ints(1).fill_(num_pages)
         self.cu_new = ints(batch + 1)
         self.slot, self.position, self._parent = ints(max_rows), ints(max_rows), ints(max_rows)
-        self._mask = torch.zeros((max_rows, -(-max_new // 64)), dtype=torch.int64, device=device)
-        self.tree_mask = None
+        self._mask = torch.zeros(max_rows * -(-max_new // 64), dtype=torch.int64, device=device)
+        self.tree_mask, self.most = None, max_new
         self._workspace = None
 
-    def plan(self, new, parent=None, stream=None) -> None:
+    def plan(self, new, parent=None, most: int | None = None) -> None:
         """Start a step in which request b adds ``new[b]`` rows (an int32 tensor [batch] on the
-        GPU): their slots and positions, and with ``parent`` (int32, one for each new row) the
-        masks of drafted trees. ``seq_len[b]`` is 0 where the pages did not suffice."""
+        GPU, at most ``most`` each; the attention is quickest when that is close): their slots and
+        positions, and with ``parent`` (int32, one for each new row) the masks of drafted trees.
+        ``seq_len[b]`` is 0 where the pages did not suffice."""
+        self.most = self.max_new if most is None else most
+        if not 1 <= self.most <= self.max_new:
+            raise ValueError(f"most must lie in 1..{self.max_new}")
         self.cu_new[1:].copy_(new.cumsum(0))
+        self.tree_mask = None
         if parent is not None:
             self._parent[:parent.numel()].copy_(parent)
-            self.tree_mask = self._mask
-        else:
-            self.tree_mask = None
+            words = -(-self.most // 64)
+            self.tree_mask = self._mask[:self.slot.numel() * words].view(-1, words)
         paged.fa_cache_plan(self.ctx_len, self.cu_new, self.block_table, self.n_pages, self.free_list, self.free_count,
-                            self.seq_len, self.slot, self.position, page_size=self.page_size, max_new=self.max_new,
-                            parent=None if parent is None else self._parent, tree_mask=self.tree_mask, stream=stream)
+                            self.seq_len, self.slot, self.position, page_size=self.page_size, max_new=self.most,
+                            parent=None if parent is None else self._parent, tree_mask=self.tree_mask)
 
-    def append(self, layer: int, q, k, v, rope: Rope | None = None, q_out=None, stream=None):
+    def append(self, layer: int, q, k, v, rope: Rope | None = None, q_out=None):
         """Write the step's rows ``k`` and ``v`` [T, H_kv, d] to their slots; returns ``q`` rotated (and
         rotates ``k``) by ``rope``. Rows past the step's last (a padded batch) are not written."""
         T = k.shape[0]
         if rope is None:
-            paged.fa_rope_append(None, k, v, None, self.k[layer], self.v[layer], self.slot[:T], stream=stream)
+            paged.fa_rope_append(None, k, v, None, self.k[layer], self.v[layer], self.slot[:T])
             return q
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
         positions = rope.positions
         if positions is None:  # the plan's, on as many axes as the tables may name
             positions = self.position[:T].expand(8, T)
         paged.fa_rope_append(q, k, v, q_out, self.k[layer], self.v[layer], self.slot[:T], positions, rope.inv_freq,
-                             rope.axis, pairs=rope.pairs, stream=stream)
+                             rope.axis, pairs=rope.pairs)
         return q_out
 
-    def attend(self, layer: int, q, o=None, lse=None, scale=None, stream=None):
+    def attend(self, layer: int, q, o=None, lse=None, scale=None):
         """Attention of the step's rows ``q`` [T, Hq, d] over the cache; returns (o, lse)."""
         T, Hq, d = q.shape
         o = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device) if o is None else o
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-        need = paged.fa_tree_fwd_workspace_size(self.batch, T, self.max_new, Hq, self.k.shape[2], d)
+        need = paged.fa_tree_fwd_workspace_size(self.batch, T, self.most, Hq, self.k.shape[2], d)
         if self._workspace is None or self._workspace.numel() < need:
             self._workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         mask = None if self.tree_mask is None else self.tree_mask[:T]
         paged.fa_tree_fwd(q, self.k[layer], self.v[layer], self.block_table, self.seq_len, self.cu_new, o, lse,
-                          self._workspace, max_q=self.max_new, tree_mask=mask, scale=scale, stream=stream)
+                          self._workspace, max_q=self.most, tree_mask=mask, scale=scale)
         return o, lse
 
-    def commit(self, accepted, n_accepted, stream=None) -> None:
+    def commit(self, accepted, n_accepted) -> None:
         """End a step of drafted trees: of each request's new rows keep the path ``accepted[b,
-        :n_accepted[b]]`` (int32, strictly increasing), in every layer."""
+        :n_accepted[b]]`` (int32, strictly increasing; none of a refused request), in every layer."""
         for layer in range(self.k.shape[0]):
             paged.fa_cache_commit(self.k[layer], self.v[layer], self.block_table, self.ctx_len, accepted, n_accepted,
-                                  self.new_len, stream=stream)
-        with torch.cuda.stream(stream):
-            self.ctx_len.copy_(self.new_len)
+                                  self.new_len)
+        self.ctx_len.copy_(self.new_len)
 
-    def keep(self, stream=None) -> None:
+    def keep(self) -> None:
         """End a step whose new rows all stay (decoding, prompt chunks); a refused request
         (``seq_len`` 0 although it has rows) keeps its length."""
-        with torch.cuda.stream(stream):
-            torch.where(self.seq_len > 0, self.seq_len, self.ctx_len, out=self.ctx_len)
+        torch.where(self.seq_len > 0, self.seq_len, self.ctx_len, out=self.ctx_len)
 
     def release(self, b: int) -> None:
         """Request b is done: its pages go back with the next plan."""

@@ -8,8 +8,10 @@
 namespace fa {
 namespace {
 
-// Columns of the MMA: the smallest tile that holds a request's rows of one cache head. With
-// head dimension 256 shared memory holds no more than 64 rows next to one stage of K and V.
+// Query rows of a unit: the smallest tile that holds a request's rows of one cache head, since a
+// wider one costs as if it were full (a tree of 64 rows over 64K keys, d = 64: 65 us with 64, 75
+// with 128; 96 rows over 4000 keys: 54 us with 128, 68 as two of 64). With head dimension 256
+// shared memory holds no more than 64 rows next to one stage of K and V.
 int row_tile(int max_q, int group, int D) {
   const long long rows = static_cast<long long>(max_q) * group;
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 || D == 256 ? 64 : 128));
@@ -17,10 +19,13 @@ int row_tile(int max_q, int group, int D) {
 
 int padded_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
 
-// Units that are many and long are not cut: a CTA each.
+// Prompt chunks with at least a unit for every SM are not cut: a CTA each, the longest first. (H_kv =
+// 8, groups of 4, d = 128: one prompt of 1024 rows 44 us cut and 27 not, 2048 rows 90 and 62, 8192
+// rows 970 and 575; 8 x 128 rows over 3000 keys 78 and 71; 4 x 300 rows over 1000 keys 50 and 51. Fewer
+// or smaller units are cut: they go with long caches, whose lengths would not even out.)
 bool by_unit(int rows, int max_q, int Hq, int H_kv, int tile) {
   const long long units = static_cast<long long>(H_kv) * ((static_cast<long long>(rows) * (Hq / H_kv) + tile - 1) / tile);
-  return static_cast<long long>(max_q) * (Hq / H_kv) >= 512 && units >= 4 * tree::kMaxWorkers;
+  return static_cast<long long>(max_q) * (Hq / H_kv) >= 512 && units >= tree::kMaxWorkers;
 }
 
 struct Workspace {

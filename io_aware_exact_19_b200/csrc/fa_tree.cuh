@@ -156,7 +156,8 @@ struct Cursor {
                                                      int& units, int& tiles) {
     q0 = min(max(cu0, 0), p.rows);
     n = max(min(cu1, p.rows) - q0, 0);
-    len = static_cast<int>(min(static_cast<long long>(max(seq, 0)), static_cast<long long>(p.max_pages) << p.page_shift));
+    const long long held = min(static_cast<long long>(p.max_pages) << p.page_shift, 0x7FFFFF00ll);  // keys stay ints
+    len = static_cast<int>(min(static_cast<long long>(max(seq, 0)), held));
     units = static_cast<int>((static_cast<long long>(n) * p.G + N - 1) / N);
     tiles = p.by_unit ? 1 : max((len + kKeys - 1) / kKeys, 1);
     return static_cast<long long>(p.H_kv) * units * tiles;
@@ -166,9 +167,15 @@ struct Cursor {
   __device__ __forceinline__ void take(const Params& p, Item& it, int q0, int n, int len, int units, int tiles) {
     const long long u = divide(off, tiles);
     const int t = static_cast<int>(off - u * tiles);
-    const int h = static_cast<int>(divide(u, units));
-    int rt = static_cast<int>(u - static_cast<long long>(h) * units);
-    if (p.by_unit) rt = units - 1 - rt;  // under a chain the last rows see the most keys
+    // Cut: head by head, its row tiles in order. By unit: under a chain the last rows see the most
+    // keys, so the last row tile of every head, then the one before, and so on.
+    int h = static_cast<int>(divide(u, p.by_unit ? p.H_kv : units));
+    int rt = static_cast<int>(u - static_cast<long long>(h) * (p.by_unit ? p.H_kv : units));
+    if (p.by_unit) {
+      const int back = h;
+      h = rt;
+      rt = units - 1 - back;
+    }
     const int r0 = rt * N, ctx = max(p.seq_len[b], 0) - n;
     const int taken = static_cast<int>(min(static_cast<long long>(tiles - t), end - pos));
     int t1 = (len + kKeys - 1) / kKeys;

@@ -21,7 +21,7 @@ class Plain:
         self.v = [[np.zeros((0, H_kv, d)) for _ in range(batch)] for _ in range(layers)]
 
 
-def _step(cache, plain, rng, new, fmt, Hq, rope, tables, accept=None, pad=0):
+def _step(cache, plain, rng, new, fmt, Hq, rope, tables, accept=None, pad=0, most=None):
     """One step of all layers; returns nothing, asserts every output. With `accept` (a function of the
     tree sizes) the new rows are drafted trees of which a path is kept."""
     layers, _, H_kv, _, d = cache.k.shape
@@ -29,7 +29,7 @@ def _step(cache, plain, rng, new, fmt, Hq, rope, tables, accept=None, pad=0):
     T = int(sum(new))
     cu = np.concatenate([[0], np.cumsum(new)])
     parents = random_parents(new, rng) if accept else None
-    cache.plan(ints(new), None if parents is None else ints(parents))
+    cache.plan(ints(new), None if parents is None else ints(parents), most=most)
     bits = [C.ancestors(parents[cu[b]:cu[b + 1]]) if accept else None for b in range(len(new))]
     pos = np.concatenate([ctx[b] + (np.arange(n) if bits[b] is None else bits[b].sum(1) - 1) for b, n in enumerate(new)])
     assert cache.position[:T].tolist() == pos.tolist()
@@ -89,9 +89,9 @@ def test_serving(fmt, d, page, H_kv, Hq, sections):
     plain = Plain(batch, layers, H_kv, d)
     args = (cache, plain, rng)
     _step(*args, [130, 1, 77, 0, 5], fmt, Hq, rope, tables)                                  # prompts
-    _step(*args, [1, 1, 1, 0, 1], fmt, Hq, rope, tables, pad=3)                              # decoding, a padded batch
-    for _ in range(2):
-        _step(*args, [9, 20, 70, 0, 3], fmt, Hq, rope, tables, accept=True)                  # drafted trees
+    _step(*args, [1, 1, 1, 0, 1], fmt, Hq, rope, tables, pad=3, most=1)                      # decoding, a padded batch
+    for most in (70, 128):
+        _step(*args, [9, 20, 70, 0, 3], fmt, Hq, rope, tables, accept=True, most=most)       # drafted trees
     cache.release(2)                                                                         # one is done, one begins
     for layer in range(layers):
         plain.k[layer][2] = plain.k[layer][2][:0]
