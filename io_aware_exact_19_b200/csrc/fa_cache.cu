@@ -13,7 +13,8 @@ namespace {
 // ------------------------------------------------------------------ plan
 //
 // Latency bound: the floor is a launch and the loads that wait for one another (lengths, free
-// pages, table). The pages are handed out by one cluster of 8 CTAs, so that the two places where
+// pages, table). Measured: 4.3 us for 8 requests' next tokens, 6.4 for 256 trees of up to 64 tokens
+// (16.5 with pages by a warp per request and the trees behind them in the same CTAs). The pages are handed out by one cluster of 8 CTAs, so that the two places where
 // all requests meet (pages given back before any is taken, tables written before slots are read)
 // are cluster barriers and the whole plan is one launch. Every CTA reads all lengths and scans
 // the needs itself, one load's latency, which is cheaper than handing prefix sums around; pages
@@ -267,7 +268,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 // it along the whole path, a batch of rows at a time (all loads of a batch before its
 // stores). The indices are strictly increasing, so a row's target never lies behind
 // the source of a later one and no order between threads is needed. It moves a few
-// rows of each request and is bound by latency: lengths, then the table, then the rows.
+// rows of each request and is bound by latency: lengths, then the table, then the rows (256
+// requests, about 6 rows of 2 x 8 heads of 128 each: 6.1 us, 13.6 MB).
 
 constexpr int kCommitThreads = 256;
 constexpr int kCommitBatch = 8;

@@ -2,9 +2,9 @@
 // cores (tcgen05), split over the keys and the requests alike.
 //
 // The rows of one request that share a cache head (its new tokens times the group of
-// query heads) are few: 1 x 4 in decoding, 48 x 7 for a drafted tree, against
+// query heads) are few: 1 x 4 in decoding, 16 x 4 for a drafted tree, against
 // thousands of keys. So the tiles are turned around: keys are the MMA's 128 rows and
-// the N = 16, 32, 64 or 128 query rows its columns, and nothing is padded to 128:
+// the N = 16, 32 or 64 query rows its columns, and nothing is padded to 128:
 //   S^T = K_j Q^T      A = K tile (K-major), B = Q; fp32 in TMEM, lane = key
 //   P^T = exp2(S^T * scale*log2(e) - m)   thread = key, column = query row
 //   O^T += V_j^T P^T   A = V tile read MN-major, B = P^T [key][row] in shared memory;
@@ -14,16 +14,26 @@
 // below 2^8, and O and the sums, kept in 32 bits, are consistent): one barrier with an
 // OR per tile decides that, and only then the column maxima are reduced across the
 // lanes. Each thread sums its own keys' P; the sums meet once, at the end.
+// P is rounded to the element type once (the tensor cores take 16 bits); the sums are of
+// the unrounded P. (More rows than 64: fa_tree_wide.cuh.)
 //
 // Work: a unit is (request, cache head, N query rows); its key tiles of 128 are laid
 // end to end with those of all other units, and each CTA (one per SM, persistent) takes
 // an equal run of them, whatever the lengths. A unit that is cut leaves partial
 // (O, log2-sum-exp) pairs which fa_tree_merge_kernel joins (the update of the interview
-// explainer, section 3.2, applied to runs of keys). Prompt chunks, whose units are many
-// and long, are not cut: a CTA per unit, the longest first.
+// explainer, section 3.2, applied to runs of keys), in the order of the keys, so the
+// result does not depend on which CTA ends first. Prompt chunks, whose units are many and
+// long, are not cut: a CTA per unit, the longest first.
 //
 // Warp roles: a softmax warpgroup for every 32 columns (a thread holds its key's scores for
 // them), then a TMA producer warp for K, the MMA warp, and a producer warp for V.
+//
+// What bounds it: reading K and V once, with few rows (64 requests of 0.8K to 8K keys, one row
+// each, H_kv = 8, groups of 4, d = 128, pages of 16: 1.05 GB in 167 us, 6.3 TB/s; the SMs finish
+// between 131 and 161 us, since they do not get equal shares of the bandwidth). With 64 rows and
+// d = 64 a tile's 32 KB arrive in 1400 cycles and its softmax and the MMAs' issue take 1600 (a
+// 64-row tree over 64K keys, 16 heads: 65 us, 4.1 TB/s). Small calls are bound by their way through
+// the roles: 1000 keys, one row, 9300 cycles, 2900 of them until the first load is on its way.
 #pragma once
 
 #include "fa_cache.h"
@@ -264,17 +274,18 @@ struct Tail {
 
 template <int D, int N>
 struct Smem {
+  static_assert(N == 16 || N == 32 || N == 64, "the wide kernel takes more");
   static constexpr int kCols = N < 32 ? N : 32;            // columns of a softmax thread
   static constexpr int kGroups = N / kCols;                // softmax warpgroups
   static constexpr int kTile = kKeys * D * 2;              // one K or V tile
   static constexpr int kChunk = kKeys * 128;               // its 64-column chunk
   static constexpr int kQ = N * D * 2;
-  static constexpr int kP = (N == 128 ? 2 : 1) * (N >= 64 ? (D == 128 && N == 64 ? 1 : 2) : 1) * kKeys * 128;
   // P of a tile while P V still reads the last one's: two buffers, of up to 32 columns side by
   // side in one chunk; one where shared memory is better spent on a third stage of K and V.
   static constexpr int kPBufs = D == 128 && N == 64 ? 1 : 2;
-  static constexpr int kPStep = N <= 32 ? 64 : (N == 128 ? 2 : 1) * kKeys * 128;  // bytes from one to the other
-  static constexpr int kStages = D == 256 ? 1 : (D == 128 ? (N == 128 ? 2 : 3) : (N == 128 ? 4 : (N == 64 ? 5 : 6)));
+  static constexpr int kPStep = N <= 32 ? 64 : kKeys * 128;  // bytes from one to the other
+  static constexpr int kP = (N == 64 ? kPBufs : 1) * kKeys * 128;
+  static constexpr int kStages = D == 256 ? 1 : (D == 128 ? 3 : (N == 64 ? 5 : 6));
   static constexpr int kQOff = 0;
   static constexpr int kPOff = kQOff + (kQ + 1023) / 1024 * 1024;
   static constexpr int kKOff = kPOff + kP;
@@ -636,9 +647,9 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
     float* ref = minus_ref + col0;
     float* red = reinterpret_cast<float*>(smem + L::kRedOff) + group * 4 * C;  // [4][C]
     float* factor = red;  // [C], each written over the column by the thread that has read it
-    // Row r of P: the group's half of its 64-column chunk, 16-byte pieces swizzled.
-    const uint32_t p_row = smem_u32(smem + L::kPOff) + (group / 2) * (kKeys * 128) + r * 128;
-    const int piece0 = (group % 2) * 4;
+    // Row r of P: the group's half of the 64 columns, 16-byte pieces swizzled.
+    const uint32_t p_row = smem_u32(smem + L::kPOff) + r * 128;
+    const int piece0 = group * 4;
     int n = 0;          // tiles seen
     float l[C];
 
@@ -906,7 +917,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         tc_fence_after();
       }
       constexpr int kOutBytes = D == 64 ? 128 : 256, kOutRows = kOutBytes / 64;
-      uint8_t* stage = smem + L::kPOff + (group / 2) * (kKeys * 128) + (group % 2) * 64;
+      uint8_t* stage = smem + L::kPOff + group * 64;
 #pragma unroll 1
       for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
         const uint32_t t_o = tmem + lanes + kTmemO + half * N + col0;
