@@ -867,7 +867,10 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
                  pack2<BF16>(x[c + 2], x[c + 3]), pack2<BF16>(x[c + 4], x[c + 5]), pack2<BF16>(x[c + 6], x[c + 7]));
         if (t >= clean && t * kKeys + (kKeys - 1) >= len) {
           // The last tile: what the page holds behind the last key may be anything, and 0 * NaN is
-          // not 0, so those rows of V are cleared.
+          // not 0, so those rows of V are cleared. (The stage's phase before this tile's must be over,
+          // or the wait would take it for this one: S of this tile says so of tile n - 2, and with a
+          // single stage it is tile n - 1 whose P V must have ended.)
+          if (S == 1 && !first) wait_tile(bar.pv_done(n - 1), ((n - 1) >> 1) & 1, ctx);
           wait_tile(bar.v_full(n % S), (n / S) & 1, ctx);
           if (key >= len && group == 0) {
             const uint32_t row = smem_u32(smem + L::kVOff + (n % S) * L::kTile) + r * 128;

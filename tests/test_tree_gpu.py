@@ -86,6 +86,21 @@ def test_many_requests_share_the_workers():
     assert_attention(p, o, lse, attention_reference(p, f64(q), 0.125))
 
 
+@pytest.mark.parametrize("d,fmt,page,Hq,H_kv,new", [(256, "fp16", 32, 56, 8, 1), (256, "bf16", 8, 16, 4, 13),
+                                                    (128, "bf16", 16, 16, 4, 13), (64, "fp16", 8, 16, 8, 70)])
+def test_last_tiles_under_load(d, fmt, page, Hq, H_kv, new):
+    # Every SM streams and each request ends inside a tile: the rows of V behind its last key are cleared
+    # while tiles before it may still be read. The same bits every time, and the oracle's values.
+    rng = np.random.default_rng(d + new)
+    p = Paged([int(x) for x in rng.integers(1100, 1387, 15)], [new] * 15, H_kv, d, page, fmt, seed=d)
+    q = queries(p, Hq)
+    o, lse = attend(p, q)
+    assert_attention(p, o, lse, attention_reference(p, f64(q), d ** -0.5))
+    for _ in range(20):
+        again = attend(p, q)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 def test_rows_that_see_nothing():
     # An all-zero mask over an empty context, a request that was refused (length 0), lengths below the new rows.
     p = Paged([0, 50, 0], [3, 2, 4], 2, 64, 16, "bf16", seed=3)
