@@ -267,7 +267,9 @@ struct Tail {
   Cursor<N> first_cur;  // the CTA's first run and where it goes on
   Item first_item;
   uint64_t bars[Bars<S>::kCount];
-  int bad_page[2 * S];  // whether a tile has a page index outside the cache
+  // Whether a tile has a page index outside the cache. While the softmax looks at tile n, S of
+  // tile n + 1 may have let go of its K, and the flag of tile n + 1 + S be written.
+  int bad_page[S + 2];
   uint32_t tmem;
   int abort_flag;
 };
@@ -495,8 +497,7 @@ __device__ __forceinline__ void load_tiles(const Params& p, Tail<N, S>& tail, co
       bad = __any_sync(0xffffffffu, bad && lane < per_tile && static_cast<long long>(t) * kKeys + lane * box_rows < it.len);
       if (!(ok = mbar_wait_warp(empty0 + 8 * s, ph, ctx))) break;
       if (lane == 0) {
-        // Twice the stages: the softmax may still look at the tile whose K this one replaces.
-        if (!is_v) tail.bad_page[issued % (2 * S)] = bad;
+        if (!is_v) tail.bad_page[issued % (S + 2)] = bad;
         mbar_arrive_expect_tx(full0 + 8 * s, kTile);
       }
       __syncwarp();
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         wait_tile(bar.s_full(n), (n >> 1) & 1, ctx);
         tc_fence_after();
         bool masked = t >= clean;
-        if (tail.bad_page[n % (2 * S)]) {
+        if (tail.bad_page[n % (S + 2)]) {
           // A page index outside the cache: its keys are not there.
           masked = true;
           if (key < len) {

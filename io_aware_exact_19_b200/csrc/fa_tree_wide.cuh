@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(608, 1)
         wait_tile(bar.s_full(n), (n >> 1) & 1, ctx);
         tc_fence_after();
         bool masked = t >= clean;
-        if (tail.bad_page[n % (2 * S)]) {
+        if (tail.bad_page[n % (S + 2)]) {
           // A page index outside the cache: its keys are not there.
           masked = true;
           const int step = min(1 << p.page_shift, 32);

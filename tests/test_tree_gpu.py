@@ -131,6 +131,25 @@ def test_bad_pages_are_not_seen():
     assert_attention(p, o, lse, ref)
 
 
+@pytest.mark.parametrize("d,fmt,new", [(256, "bf16", 1), (256, "fp16", 9), (64, "bf16", 40)])
+def test_bad_pages_of_a_long_run_stay_with_their_tiles(d, fmt, new):
+    # Tiles with and without a bad page in turn, one after the other on one CTA.
+    p = Paged([5000] * 20, [new] * 20, 8, d, 32, fmt, seed=d)
+    q = queries(p, 8)
+    table = p.table.clone()
+    table[:, 1::8] = -1  # of tiles 0, 2, 4, ... the second page
+    o, lse = attend(p, q, table=table)
+    n = 5000 + new
+    seen = C.seen_keys(new, n) & (np.arange(n) // 32 % 8 != 1)
+    for b in (0, 7, 19):
+        at = slice(b * new, (b + 1) * new)
+        ref = C.tree_attention(f64(q[at]), p.rows_of(p.k, b), p.rows_of(p.v, b), d ** -0.5, seen)
+        assert_attention(p, o[at], lse[at], [ref])
+    for _ in range(5):
+        again = attend(p, q, table=table)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 def test_table_shorter_than_the_length():
     # seq_len claims more rows than max_pages holds: what the table holds is seen.
     p = Paged([40], [1], 1, 64, 16, "bf16", spare=0, seed=6)
