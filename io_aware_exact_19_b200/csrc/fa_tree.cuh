@@ -921,7 +921,12 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         tc_fence_after();
       }
       constexpr int kOutBytes = D == 64 ? 128 : 256, kOutRows = kOutBytes / 64;
-      uint8_t* stage = smem + L::kPOff + group * 64;
+      // Byte `at` of column c's output: in the group's own pieces of P, since the other group may be
+      // writing P of the next item's first tile already.
+      auto staged = [&](int c, int at) {
+        const int row = c * kOutRows + at / 64;
+        return smem + L::kPOff + row * 128 + ((piece0 + at % 64 / 16) ^ (row % 8)) * 16 + at % 16;
+      };
 #pragma unroll 1
       for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
         const uint32_t t_o = tmem + lanes + kTmemO + half * N + col0;
@@ -947,12 +952,12 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
             for (int i = 0; i < 16; ++i)
               if (c + i < left) part[i * D] = __uint_as_float(o[i]);
           } else {
-            // Turned around through the group's part of P, free by now: 64 bytes of each of its
-            // 128 rows, kOutRows of them for a column's kOutBytes.
+            // Turned around through the group's part of P, free by now: its four pieces of each of
+            // the 128 rows, kOutRows rows for a column's kOutBytes.
             const int at = e % (kOutBytes / 2) * 2;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<uint16_t*>(stage + ((c + i) * kOutRows + at / 64) * 128 + at % 64) =
+              *reinterpret_cast<uint16_t*>(staged(c + i, at)) =
                   static_cast<uint16_t>(pack2<BF16>(__uint_as_float(o[i]), 0.0f));
           }
         }
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
 #pragma unroll 2
           for (int v = gt; v < C * kVecs; v += 128) {
             const int c = v / kVecs, at = v % kVecs * 16, rr = it.r0 + col0 + c;
-            const uint4 y = *reinterpret_cast<const uint4*>(stage + (c * kOutRows + at / 64) * 128 + at % 64);
+            const uint4 y = *reinterpret_cast<const uint4*>(staged(c, at));
             const int d0 = half * 128 + at / 2;
             if (c < left && d0 < p.d) {
               const int tok = p.by_group(rr), g = rr - tok * p.G;

@@ -101,6 +101,20 @@ def test_last_tiles_under_load(d, fmt, page, Hq, H_kv, new):
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("d,fmt,Hq,H_kv,new", [(64, "bf16", 16, 16, 40), (128, "fp16", 16, 16, 64),
+                                                (256, "bf16", 16, 16, 50), (64, "fp16", 40, 8, 12)])
+def test_short_units_of_two_groups(d, fmt, Hq, H_kv, new):
+    # Units of 33 to 64 rows and a tile or two, many to a CTA: one group of 32 rows hands over its
+    # output while the other begins the next unit.
+    p = Paged([int(x) for x in np.random.default_rng(d).integers(0, 150, 40)], [new] * 40, H_kv, d, 16, fmt, seed=d)
+    q = queries(p, Hq)
+    o, lse = attend(p, q)
+    assert_attention(p, o, lse, attention_reference(p, f64(q), d ** -0.5))
+    for _ in range(50):
+        again = attend(p, q)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 def test_rows_that_see_nothing():
     # An all-zero mask over an empty context, a request that was refused (length 0), lengths below the new rows.
     p = Paged([0, 50, 0], [3, 2, 4], 2, 64, 16, "bf16", seed=3)
