@@ -82,7 +82,7 @@ class PagedCache:
         self.slot, self.position, self._parent = ints(max_rows), ints(max_rows), ints(max_rows)
         self._mask = torch.zeros(max_rows * -(-max_new // 64), dtype=torch.int64, device=device)
         self.tree_mask, self.most = None, max_new
-        self._workspace = None
+        self._workspace = {}
 
     def plan(self, new, parent=None, most: int | None = None) -> None:
         """Start a step in which request b adds ``new[b]`` rows (an int32 tensor [batch] on the
@@ -122,12 +122,15 @@ class PagedCache:
         T, Hq, d = q.shape
         o = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device) if o is None else o
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-        need = paged.fa_tree_fwd_workspace_size(self.batch, T, self.most, Hq, self.k.shape[2], d)
-        if self._workspace is None or self._workspace.numel() < need:
-            self._workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        # One for each number of heads, large enough for any step and never replaced: a graph captured
+        # with a step of few rows goes on using it after one of many.
+        workspace = self._workspace.get(Hq)
+        if workspace is None:
+            need = paged.fa_tree_fwd_workspace_size(self.batch, self.slot.numel(), self.max_new, Hq, self.k.shape[2], d)
+            workspace = self._workspace[Hq] = torch.empty(need, dtype=torch.uint8, device=q.device)
         mask = None if self.tree_mask is None else self.tree_mask[:T]
         paged.fa_tree_fwd(q, self.k[layer], self.v[layer], self.block_table, self.seq_len, self.cu_new, o, lse,
-                          self._workspace, max_q=self.most, tree_mask=mask, scale=scale)
+                          workspace, max_q=self.most, tree_mask=mask, scale=scale)
         return o, lse
 
     def commit(self, accepted, n_accepted) -> None:

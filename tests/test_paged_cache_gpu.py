@@ -165,6 +165,39 @@ def test_a_step_in_a_graph():
         assert cache.ctx_len.tolist() == want[i][2]
 
 
+def test_a_captured_step_outlives_a_larger_one():
+    # Steps of one row and of many share a workspace: the larger one, coming later, must not move it.
+    cache = fa.PagedCache(num_pages=64, page_size=16, batch=2, max_len=400, H_kv=1, d=64, max_rows=300, max_new=150)
+    x = torch.randn((300, 4, 64), device="cuda").to(torch.bfloat16)
+    cache.plan(ints([100, 60]))
+    cache.append(0, x[:160], x[:160, :1], x[:160, 1:2])
+    cache.keep()
+    o, lse = torch.zeros_like(x[:2]), torch.zeros((2, 4), device="cuda")
+
+    def step():
+        cache.plan(n, most=1)
+        cache.append(0, x[:2], x[:2, :1], x[:2, 1:2])
+        cache.attend(0, x[:2], o=o, lse=lse)
+
+    n = ints([1, 1])
+    step()
+    torch.cuda.synchronize()
+    want = o.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    held = {h: w.data_ptr() for h, w in cache._workspace.items()}
+    cache.plan(ints([150, 150]))
+    cache.append(0, x, x[:, :1], x[:, 1:2])
+    cache.attend(0, x)
+    assert held == {h: w.data_ptr() for h, w in cache._workspace.items()}
+    torch.cuda.synchronize()
+    o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == fa.FA_OK and torch.equal(o, want)
+
+
 @pytest.mark.parametrize("B,H,N,d,axes,causal", [(1, 2, 300, 64, 1, True), (2, 3, 200, 128, 3, False), (1, 2, 129, 96, 2, True)])
 def test_training_with_rotary_positions(B, H, N, d, axes, causal):
     c = Case(B, H, N, d, "bf16", seed=N)
