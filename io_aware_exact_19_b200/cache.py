@@ -135,7 +135,9 @@ class PagedCache:
 
     def commit(self, accepted, n_accepted) -> None:
         """End a step of drafted trees: of each request's new rows keep the path ``accepted[b,
-        :n_accepted[b]]`` (int32, strictly increasing; none of a refused request), in every layer."""
+        :n_accepted[b]]`` (int32, strictly increasing), in every layer. A refused request, whose rows
+        were not written, keeps its length whatever they say."""
+        n_accepted = torch.where(self.seq_len > 0, n_accepted, 0)
         for layer in range(self.k.shape[0]):
             paged.fa_cache_commit(self.k[layer], self.v[layer], self.block_table, self.ctx_len, accepted, n_accepted,
                                   self.new_len)

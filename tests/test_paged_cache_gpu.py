@@ -119,6 +119,22 @@ def test_a_refused_request_waits():
     assert cache.seq_len.tolist() == [0, 40] and cache.free_count.item() == 1
 
 
+def test_a_refused_draft_keeps_nothing():
+    # Its pages would hold the first of the rows that it claims, but no row was written.
+    cache = fa.PagedCache(num_pages=2, page_size=16, batch=2, max_len=64, H_kv=1, d=64, max_rows=50, max_new=40)
+    x = torch.randn((50, 1, 64), device="cuda").to(torch.bfloat16)
+    cache.plan(ints([5, 5]))
+    cache.append(0, x[:10], x[:10], x[:10])
+    cache.keep()
+    before = cache.k.clone()
+    cache.plan(ints([4, 30]), parent=ints([-1, 0, 1, 0] + list(range(-1, 29))))
+    cache.append(0, x[:34], x[:34], x[:34])
+    assert cache.seq_len.tolist() == [9, 0]
+    second = cache.block_table[1, 0].item()
+    cache.commit(ints([[0, 3], [0, 1]]), ints([2, 2]))
+    assert cache.ctx_len.tolist() == [7, 5] and torch.equal(cache.k[:, second, :, :5], before[:, second, :, :5])
+
+
 def test_a_step_in_a_graph():
     # Captured once, replayed while the sequences grow; the same steps run eagerly give the same bits.
     def make():
