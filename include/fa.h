@@ -250,8 +250,8 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* v8, float q_sca
  * A paged cache. Row r of page p, head h starts at element
  * p*page_stride + h*head_stride + r*row_stride of k and of v (so pages laid out
  * [head][row][d] or [row][head][d], and one layer of a larger pool, are all
- * reachable). k, v: DEVICE, 16-byte aligned; the strides are positive multiples
- * of 8 elements; page_size is a power of two, 8..1024; d as for the forward
+ * reachable). k, v: DEVICE, 16-byte aligned; the strides are multiples of 8
+ * elements, at least d; page_size is a power of two, 8..1024; d as for the forward
  * entry points; num_pages * page_size <= 2^31 - 1.
  */
 typedef struct {
@@ -266,7 +266,8 @@ typedef struct {
  * Packed rows [rows][heads][d]: head h of row t starts at element
  * t*row_stride + h*head_stride; its d elements are contiguous. DEVICE, 16-byte
  * aligned, strides multiples of 8 elements (a slice of a fused projection is
- * fine).
+ * fine; an input's may be 0 where rows or heads are shared, an output's are at
+ * least d where there is more than one).
  */
 typedef struct {
   void* data;
@@ -320,8 +321,8 @@ fa_status fa_cache_plan(int B, int rows, int max_new, int page_size, int num_pag
  * inverse != 0 turns back: the rotation is orthogonal, so this is also its
  * gradient. Angles are reduced in 64 bits, so far positions lose nothing.
  * x, out [B, H, N, d] with element strides of b, h and n (multiples of 8; the d
- * elements contiguous; 16-byte aligned); out may be x itself, but must not overlap
- * it in another way. positions int32 [n_axes][B][N] with element strides of axis and
+ * elements contiguous; 16-byte aligned; those of out at least d where there is more
+ * than one); out may be x itself, but must not overlap it in another way. positions int32 [n_axes][B][N] with element strides of axis and
  * b (0: shared by the batch); inv_freq fp32 [rot/2]; axis uint8 [rot/2], an entry
  * >= n_axes leaves its pair unturned. rot a multiple of 16, 16..d; 1 <= n_axes <= 8;
  * d as for the forward entry points.
@@ -374,10 +375,11 @@ fa_status fa_tree_fwd(const fa_kv_cache* cache, const fa_rows* q, const fa_rows*
 /*
  * Keeps the accepted path of each request's draft: row ctx_len[b] + accepted[b][j] of
  * the cache moves to row ctx_len[b] + j, for j < n_accepted[b], and new_len[b] =
- * ctx_len[b] + the rows kept (a request that fa_cache_plan refused accepts none). accepted int32 [B][max_accept] holds request-local
- * indices of new tokens, strictly increasing (a path from the root is); the path ends
- * before the first entry that is not larger than the one before (or is negative), or
- * whose row has no page in the table. new_len may be ctx_len. DEVICE pointers; ctx_len,
+ * ctx_len[b] + the rows kept (a request that fa_cache_plan refused accepts none: its
+ * n_accepted has to be 0, since nothing was written). accepted int32 [B][max_accept]
+ * holds request-local indices of new tokens, strictly increasing (a path from the root
+ * is); the path ends before the first entry that is not larger than the one before (or
+ * is negative), or whose row has no page in the table. new_len may be ctx_len. DEVICE pointers; ctx_len,
  * n_accepted, new_len int32 [B]. One launch.
  */
 fa_status fa_cache_commit(const fa_kv_cache* cache, int B, int max_pages, int max_accept, const int32_t* block_table,

@@ -18,6 +18,9 @@ int page_shift_of(int page_size) {
 
 bool stride_ok(long long s) { return s > 0 && s % 8 == 0 && s < (1ll << 38); }
 
+// Rows of d elements, `count` of them `stride` apart, do not overlap (what is written must not).
+bool apart(long long stride, long long count, int d) { return count <= 1 || stride >= d; }
+
 fa_status check_cache(const fa_kv_cache* c) {
   if (c == nullptr || !aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID_ARG;
   if (c->dtype != FA_FP16 && c->dtype != FA_BF16) return FA_ERR_INVALID_ARG;
@@ -25,12 +28,19 @@ fa_status check_cache(const fa_kv_cache* c) {
   if (!stride_ok(c->page_stride) || !stride_ok(c->head_stride) || !stride_ok(c->row_stride)) return FA_ERR_INVALID_ARG;
   if (!fa::head_dim_supported(c->d) || c->H_kv > 65535) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(c->num_pages) * c->page_size > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+  if (!apart(c->page_stride, c->num_pages, c->d) || !apart(c->head_stride, c->H_kv, c->d) ||
+      !apart(c->row_stride, c->page_size, c->d))
+    return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
 bool rows_ok(const fa_rows* r) {
   return r != nullptr && aligned(r->data, 16) && r->row_stride >= 0 && r->row_stride % 8 == 0 &&
          r->head_stride >= 0 && r->head_stride % 8 == 0;
+}
+
+bool written_rows_ok(const fa_rows* r, int rows, int heads, int d) {
+  return rows_ok(r) && apart(r->row_stride, rows, d) && apart(r->head_stride, heads, d);
 }
 
 fa_status check_batch(int B, int rows, int max_pages) {
@@ -63,7 +73,7 @@ fa_status tree_impl(const fa_kv_cache* cache, const fa_rows* q, const fa_rows* o
   if (Hq > 65535 || (tree_mask != nullptr && max_q > FA_TREE_MAX)) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(rows) * Hq > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
   if (rows == 0) return FA_OK;
-  if (!rows_ok(q) || !rows_ok(o) || !aligned(lse, 4)) return FA_ERR_INVALID_ARG;
+  if (!rows_ok(q) || !written_rows_ok(o, rows, Hq, cache->d) || !aligned(lse, 4)) return FA_ERR_INVALID_ARG;
   if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(seq_len, 4)) return FA_ERR_INVALID_ARG;
   if (tree_mask != nullptr && !aligned(tree_mask, 8)) return FA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return FA_ERR_INVALID_ARG;
@@ -148,6 +158,8 @@ fa_status fa_rope(fa_dtype dtype, const void* x, void* out, int B, int H, int N,
   for (int i = 0; i < 3; ++i)
     if (x_strides[i] < 0 || x_strides[i] % 8 != 0 || out_strides[i] < 0 || out_strides[i] % 8 != 0)
       return FA_ERR_INVALID_ARG;
+  if (!apart(out_strides[0], B, d) || !apart(out_strides[1], H, d) || !apart(out_strides[2], N, d))
+    return FA_ERR_INVALID_ARG;
   const fa_status s = check_rope_tables(n_axes, rot, d, positions, pos_axis_stride, inv_freq, axis);
   if (s != FA_OK) return s;
   fa::RopeArgs a{};
@@ -188,7 +200,7 @@ fa_status fa_rope_append(const fa_kv_cache* cache, int rows, int Hq, const fa_ro
   if (rows < 0 || (q == nullptr) != (q_out == nullptr)) return FA_ERR_INVALID_ARG;
   if (rows == 0) return FA_OK;
   if (!rows_ok(k) || !rows_ok(v) || !aligned(slot, 4)) return FA_ERR_INVALID_ARG;
-  if (q != nullptr && (Hq < 1 || !rows_ok(q) || !rows_ok(q_out))) return FA_ERR_INVALID_ARG;
+  if (q != nullptr && (Hq < 1 || !rows_ok(q) || !written_rows_ok(q_out, rows, Hq, cache->d))) return FA_ERR_INVALID_ARG;
   if (q != nullptr && Hq > 65535) return FA_ERR_UNSUPPORTED;
   s = check_rope_tables(n_axes, rot, cache->d, positions, pos_axis_stride, inv_freq, axis);
   if (s != FA_OK) return s;

@@ -114,6 +114,16 @@ def test_tree_refusals(lib):
         assert size(*bad) == 0
 
 
+def test_outputs_that_overlap_themselves(lib):
+    for kw in (dict(page_stride=56), dict(head_stride=8), dict(row_stride=56)):
+        c = cache(**kw)
+        assert append(lib, c) == tree(lib, c) == INVALID, kw
+    for kw in (dict(os=(384, 192, 0)), dict(os=(384, 0, 64)), dict(B=2, os=(0, 192, 64)), dict(os=(384, 192, 56))):
+        assert rope(lib, **kw) == INVALID, kw
+    for bad in (rows(row=0), rows(head=0), rows(head=56)):
+        assert append(lib, qo=bad) == INVALID and tree(lib, o=bad) == INVALID
+
+
 def test_commit_refusals(lib):
     def commit(c=None, B=2, width=3, acc=4, table=P, ctx=P, a=P, n=P, out=P):
         return lib.fa_cache_commit(ctypes.byref(c or cache()), B, width, acc, table, ctx, a, n, out, None)
