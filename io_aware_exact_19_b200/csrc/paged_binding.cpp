@@ -55,6 +55,12 @@ double real(PyObject* o) {
   return v;
 }
 
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();
+  return v;
+}
+
 int device_of(const at::Tensor& t, const char* name) {
   if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(name) + ": expected a CUDA tensor, got " + text(t));
   return t.get_device();
@@ -230,7 +236,7 @@ PyObject* rope(PyObject* const* a) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   return PyLong_FromLong(call_rope(dtype, x.data_ptr(), out.data_ptr(), size(B), size(x.size(1)), size(N), size(x.size(3)),
                                    xs, os, t.positions, t.axis_stride, shared ? 0 : pos.stride(1), t.axes, t.inv_freq,
-                                   t.axis, t.rot, PyObject_IsTrue(a[5]), PyObject_IsTrue(a[6]), stream_of(a[7], dev)));
+                                   t.axis, t.rot, truth(a[5]), truth(a[6]), stream_of(a[7], dev)));
 }
 
 // q, k, v, q_out, cache_k, cache_v, slot, positions, inv_freq, axis, pairs, stream
@@ -258,7 +264,7 @@ PyObject* append(PyObject* const* a) {
   const int32_t* slot = ints(a[6], "slot", dev);
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   return PyLong_FromLong(call_append(&cache.c, size(T), heads, with_q ? &q : nullptr, &k, &v, with_q ? &q_out : nullptr, slot,
-                                     t.positions, t.axis_stride, t.axes, t.inv_freq, t.axis, t.rot, PyObject_IsTrue(a[10]),
+                                     t.positions, t.axis_stride, t.axes, t.inv_freq, t.axis, t.rot, truth(a[10]),
                                      stream_of(a[11], dev)));
 }
 

@@ -137,3 +137,10 @@ def test_append_without_queries_and_in_place():
     torch.cuda.synchronize()
     assert_rotated(q, C.rope(f64(x), pos[:, :, None], inv, axis), f64(x), "bf16")
     assert torch.equal(ck[1, :, 1], q[1])
+
+
+def test_flags_without_a_truth_value_are_refused():
+    x = torch.zeros((1, 1, 2, 32), dtype=torch.float16, device="cuda")
+    _, _, inv_d, axis_d = tables(32, 1)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        fa.fa_rope(x, x, ints([[0, 1]]), inv_d, axis_d, inverse=torch.zeros(2))
