@@ -1010,22 +1010,32 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
   if (rr >= u.z * p.G) return;
   const int pieces = a.z - w + 1;
   auto row_of = [&](int i) { return static_cast<size_t>(i == 0 ? a.y : 2 * (w + i)) * N + c; };
-  // A lane holds the lse of one piece, of 32 at a time, and kPer consecutive elements of O. The
-  // first pieces' O is asked for together with the lse's, before their weights are known.
-  constexpr int kPer = D / 32, kFirst = 8;
-  float o[kFirst][kPer];
-  auto load_o = [&](int i, float (&to)[kPer]) {
-    const float2* src = reinterpret_cast<const float2*>(p.part_o + row_of(i) * D + lane * kPer);
+  // A lane holds the lse of one piece, of 32 at a time, and kPer consecutive elements of O, of kAhead
+  // pieces at a time; the first are asked for together with the lse's, before their weights are known.
+  // (Many rows come in few pieces: 16 trees of 48 x 7 rows took 60 us with eight ahead, 57 with four; four
+  // rows to a warp, in a quarter of the blocks, 57 there and 38 for 33 in a tree over 30000 keys.)
+  constexpr int kPer = D / 32, kAhead = N >= 64 ? 4 : 8;
+  float o[kAhead][kPer];
+  auto load_o = [&](int i0) {
 #pragma unroll
-    for (int k = 0; k < kPer; k += 2) {
-      const float2 y = src[k / 2];
-      to[k] = y.x;
-      to[k + 1] = y.y;
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i < pieces) {
+        const float* src = p.part_o + row_of(i0 + i) * D + lane * kPer;
+        if constexpr (kPer == 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          o[i][0] = y.x, o[i][1] = y.y;
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; k += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src + k);
+            o[i][k] = y.x, o[i][k + 1] = y.y, o[i][k + 2] = y.z, o[i][k + 3] = y.w;
+          }
+        }
+      }
     }
   };
   float x = lane < pieces ? p.part_lse[row_of(lane)] : -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kFirst; ++i) load_o(min(i, pieces - 1), o[i]);
+  load_o(0);
   float m = x;
   bool nan = x != x;
   for (int i = lane + 32; i < pieces; i += 32) {
@@ -1038,28 +1048,19 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
   float z = 0.0f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
-  auto add = [&](float f, const float (&y)[kPer]) {
-    z += f;
+  for (int i0 = 0; i0 < pieces; i0 += kAhead) {
+    if (i0 > 0) {
+      load_o(i0);
+      if (i0 % 32 == 0) x = i0 + lane < pieces ? p.part_lse[row_of(i0 + lane)] : -INFINITY;
+    }
+    const float weight = x == -INFINITY ? 0.0f : ex2(x - m);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = fmaf(f, y[k], acc[k]);
-  };
-  if (m != -INFINITY || nan) {
-    for (int i0 = 0; i0 < pieces; i0 += 32) {
-      if (i0 > 0) x = i0 + lane < pieces ? p.part_lse[row_of(i0 + lane)] : -INFINITY;
-      const float weight = x == -INFINITY ? 0.0f : ex2(x - m);
-      const int here = min(32, pieces - i0);
-      if (i0 == 0) {
+    for (int i = 0; i < kAhead; ++i) {
+      const float f = __shfl_sync(0xffffffffu, weight, (i0 + i) % 32);
+      if (i0 + i < pieces) {
+        z += f;
 #pragma unroll
-        for (int i = 0; i < kFirst; ++i) {
-          const float f = __shfl_sync(0xffffffffu, weight, i);
-          if (i < here) add(f, o[i]);
-        }
-      }
-#pragma unroll 4
-      for (int i = i0 == 0 ? kFirst : 0; i < here; ++i) {
-        float y[kPer];
-        load_o(i0 + i, y);
-        add(__shfl_sync(0xffffffffu, weight, i), y);
+        for (int k = 0; k < kPer; ++k) acc[k] = fmaf(f, o[i][k], acc[k]);
       }
     }
   }
