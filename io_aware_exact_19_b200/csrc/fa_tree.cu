@@ -19,7 +19,7 @@ int row_tile(int max_q, int group, int D) {
 
 int padded_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
 
-// Prompt chunks with at least a unit for every SM are not cut: a CTA each, the longest first. (H_kv =
+// Prompt chunks with at least a unit for every SM are not cut: whole units, the longest first. (H_kv =
 // 8, groups of 4, d = 128: one prompt of 1024 rows 44 us cut and 27 not, 2048 rows 90 and 62, 8192
 // rows 970 and 575; 8 x 128 rows over 3000 keys 78 and 71; 4 x 300 rows over 1000 keys 50 and 51. Fewer
 // or smaller units are cut: they go with long caches, whose lengths would not even out.)
@@ -112,10 +112,18 @@ int launch_t(const TreeArgs& a, cudaStream_t stream) {
   }
   cudaError_t e = host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return static_cast<int>(e);
-  // By unit: request b has at most H_kv * (its rows / N rounded up) units.
-  const long long grid = p.by_unit ? static_cast<long long>(p.H_kv) *
-                                         ((static_cast<long long>(a.rows) * p.G + N - 1) / N + a.B)
-                                   : p.workers;
+  // By unit: request b has at most H_kv * (its rows / N rounded up) units. With eight units a worker and
+  // more, the workers take them in turn, which spares each unit a CTA's start (39 prompts of 485 rows x 7
+  // behind 36, H_kv = 3, d = 128: 226 us with a CTA for each, 174; 45 of 471 x 4, d = 64: 135 and 101; one of
+  // 8192 rows 585 and 561; 24 of 500 x 4 behind up to 4000 443 and 417); with fewer, of any lengths, whichever
+  // CTA is free takes the next (10 of 300 x 4 behind up to 4000, four a worker: 131 us, in turn 143; 16 behind
+  // up to 6000, seven a worker: 270 and 285).
+  long long grid = p.workers;
+  if (p.by_unit) {
+    const long long whole = static_cast<long long>(p.H_kv) * ((static_cast<long long>(a.rows) * p.G + N - 1) / N);
+    const long long most = whole + static_cast<long long>(p.H_kv) * a.B;
+    if (whole < 8ll * p.workers) grid = most;
+  }
   kern<<<static_cast<unsigned>(grid), kThreads, kSmem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.by_unit) return static_cast<int>(e);

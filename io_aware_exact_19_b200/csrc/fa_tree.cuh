@@ -23,7 +23,7 @@
 // (O, log2-sum-exp) pairs which fa_tree_merge_kernel joins (the update of the interview
 // explainer, section 3.2, applied to runs of keys), in the order of the keys, so the
 // result does not depend on which CTA ends first. Prompt chunks, whose units are many and
-// long, are not cut: a CTA per unit, the longest first.
+// long, are not cut: each CTA takes whole units, the longest first.
 //
 // Warp roles: a softmax warpgroup for every 32 columns (a thread holds its key's scores for
 // them), then a TMA producer warp for K, the MMA warp, and a producer warp for V.
@@ -76,7 +76,7 @@ struct Params {
   const int32_t* seq_len;
   const unsigned long long* tree_mask;
   float scale_log2;
-  int by_unit;      // a CTA per unit (no cuts)
+  int by_unit;      // no cuts: CTA c takes units c, c + gridDim.x, ...
   int workers;      // CTAs the key tiles are cut among
   float* part_o;    // fp32 [2 * workers][N][D]
   float* part_lse;  // fp32 [2 * workers][N], log2 units
@@ -211,8 +211,8 @@ struct Cursor {
     it.take = taken;
     it.tiles = tiles;
     it.valid = 1;
-    pos += taken;
-    off += taken;
+    pos += p.by_unit ? gridDim.x : taken;
+    off += p.by_unit ? gridDim.x : taken;
   }
 
   __device__ __forceinline__ void next(const Params& p, Item& it) {
@@ -432,7 +432,7 @@ __device__ __forceinline__ Start begin(const Params& p, Tail<N, S>& tail, const 
     }
     share.set(total, p.by_unit ? max(total, 1ll) : p.workers);
     lo = share.begin(blockIdx.x);
-    const long long hi = share.begin(static_cast<long long>(blockIdx.x) + 1);
+    const long long hi = p.by_unit ? total : share.begin(static_cast<long long>(blockIdx.x) + 1);
     if (p.B <= kThreads) {
       if (lo < hi && mine <= lo && lo < mine + w) {
         Cursor<N> c{lo, hi, lo - mine, tid};

@@ -115,6 +115,20 @@ def test_short_units_of_two_groups(d, fmt, Hq, H_kv, new):
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("d,fmt,Hq,H_kv,new", [(64, "bf16", 32, 16, [400, 300, 0, 450] * 5), (256, "fp16", 16, 8, [260] * 20),
+                                                (128, "bf16", 40, 8, [128, 0, 1, 260, 300] * 6)])
+def test_whole_units_in_turn(d, fmt, Hq, H_kv, new):
+    # Several whole units a CTA, with requests of none and of one between them.
+    p = Paged([int(x) for x in np.random.default_rng(d).integers(0, 300, len(new))], new, H_kv, d, 16, fmt, seed=d)
+    q = queries(p, Hq, p.T + 9)
+    o, lse = attend(p, q)
+    assert_attention(p, o, lse, attention_reference(p, f64(q), d ** -0.5))
+    assert torch.isnan(o[p.T:]).all() and torch.isnan(lse[p.T:]).all()
+    for _ in range(3):
+        again = attend(p, q)
+        assert torch.equal(o[:p.T], again[0][:p.T]) and torch.equal(lse[:p.T], again[1][:p.T])
+
+
 def test_rows_that_see_nothing():
     # An all-zero mask over an empty context, a request that was refused (length 0), lengths below the new rows.
     p = Paged([0, 50, 0], [3, 2, 4], 2, 64, 16, "bf16", seed=3)
