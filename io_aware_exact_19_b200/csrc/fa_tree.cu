@@ -21,7 +21,7 @@ int padded_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
 
 // Prompt chunks with at least a unit for every SM are not cut: whole units, the longest first. (H_kv =
 // 8, groups of 4, d = 128: one prompt of 1024 rows 44 us cut and 27 not, 2048 rows 90 and 62, 8192
-// rows 970 and 575; 8 x 128 rows over 3000 keys 78 and 71; 4 x 300 rows over 1000 keys 50 and 51. Fewer
+// rows 970 and 566; 8 x 128 rows over 3000 keys 78 and 71; 4 x 300 rows over 1000 keys 50 and 51. Fewer
 // or smaller units are cut: they go with long caches, whose lengths would not even out.)
 bool by_unit(int rows, int max_q, int Hq, int H_kv, int tile) {
   const long long units = static_cast<long long>(H_kv) * ((static_cast<long long>(rows) * (Hq / H_kv) + tile - 1) / tile);

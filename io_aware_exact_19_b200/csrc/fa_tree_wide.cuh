@@ -19,7 +19,7 @@
 //
 // A tile of 128 keys takes 2100 cycles at d = 128 (the MMAs 1024, the exponentials 1024): two chunks of
 // 2048 rows behind 8192 keys, H_kv = 8, groups of 4: 583 us, 988 TFLOP/s (of 1653 measured for a plain
-// product; under the power cap, back to back, 630 to 670 us); one prompt of 8192 rows 575 us, 910
+// product; under the power cap, back to back, 630 to 670 us); one prompt of 8192 rows 566 us, 930
 // TFLOP/s. Tried and slower: two sets of eight warps taking the tiles in turn, each with its own O (1960
 // cycles a tile, but more to join at the end: the same on chunks, 64 for 60 us on 16 trees of 48 x 7
 // rows); P computed before the vote; a quarter to a half of the exponentials as polynomials on the FMA
