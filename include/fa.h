@@ -284,8 +284,9 @@ typedef struct {
  *   2. Requests that need more take them from the end of the free list, in the order
  *      of the requests. Request b is granted iff it needs none, or the needs of
  *      requests 0..b together do not exceed the free pages. A request whose
- *      ctx_len is negative, whose n_b is negative or over max_new, or which needs
- *      more than max_pages pages, takes no part and is refused.
+ *      ctx_len is negative, whose n_b is negative or over max_new, whose new rows do
+ *      not all lie in 0 .. rows-1, or which needs more than max_pages pages, takes no
+ *      part and is refused.
  *   3. Granted: n_pages[b] and block_table row b are updated and seq_len[b] =
  *      ctx_len[b] + n_b. Refused: pages and table stay, seq_len[b] = 0.
  *   4. slot[cu_new[b] + i] = row ctx_len[b] + i as page * page_size + row in page, -1

@@ -88,7 +88,8 @@ class PagedCache:
         """Start a step in which request b adds ``new[b]`` rows (an int32 tensor [batch] on the
         GPU, at most ``most`` each; the attention is quickest when that is close): their slots and
         positions, and with ``parent`` (int32, one for each new row) the masks of drafted trees.
-        ``seq_len[b]`` is 0 where the pages did not suffice."""
+        ``seq_len[b]`` is 0 where the pages did not suffice, and where a request's rows go beyond the
+        step's ``max_rows``."""
         self.most = self.max_new if most is None else most
         if not 1 <= self.most <= self.max_new:
             raise ValueError(f"most must lie in 1..{self.max_new}")

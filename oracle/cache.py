@@ -39,7 +39,8 @@ def plan(ctx, cu, table, held, free, free_count, page, rows, max_new, parent=Non
     for b in range(B):
         n = cu[b + 1] - cu[b]
         w = -(-(ctx[b] + n) // page)
-        want.append(w if ctx[b] >= 0 and 0 <= n <= max_new and w <= max_pages else None)
+        inside = n == 0 or (cu[b] >= 0 and cu[b + 1] <= rows)
+        want.append(w if ctx[b] >= 0 and 0 <= n <= max_new and inside and w <= max_pages else None)
     count = free_count
     for b in range(B):
         if want[b] is not None:
@@ -65,7 +66,7 @@ def plan(ctx, cu, table, held, free, free_count, page, rows, max_new, parent=Non
     for b in range(B):
         n = cu[b + 1] - cu[b]
         up = None if parent is None else ancestors(parent[cu[b]:cu[b] + n])
-        for i in range(n):
+        for i in range(min(n, rows - cu[b])):
             t, at = cu[b] + i, ctx[b] + i
             if granted[b]:
                 slot[t] = table[b][at // page] * page + at % page

@@ -1,0 +1,76 @@
+"""Steps whose rows do not fit the buffers they are given, and PagedCache's optional buffers."""
+import numpy as np
+import pytest
+import torch
+
+import io_aware_exact_19_b200 as fa
+from tests.cache_cases import ints, random_parents
+from tests.test_cache_gpu import State
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("new,rows", [([8, 8, 8], 20), ([8, 8, 8], 16), ([30, 1, 0], 29), ([5, 0, 9, 0, 1], 13), ([3], 0)])
+def test_plan_refuses_rows_behind_the_buffers(new, rows, tree):
+    st = State(len(new), 8, 40)
+    parent = random_parents(new, np.random.default_rng(rows))[:rows] if tree else None
+    ctx = [3 * b for b in range(len(new))]
+    st.step(ctx, [0] * len(new), 8, 32, rows, [-1] * rows if tree else None)  # pages of the cached rows
+    seq = st.step(ctx, new, 8, 32, rows, parent)
+    ends = np.cumsum(new)
+    assert seq == [c + n if n == 0 or e <= rows else 0 for c, n, e in zip(ctx, new, ends)]
+
+
+def test_plan_refuses_broken_offsets_and_writes_inside():
+    # Offsets that fall or point outside the rows: the requests outside are refused, no page is lost or given
+    # out twice, and nothing around the outputs is written.
+    for cu, seq_want in (([-5, -2, 1, 4], [0, 0, 4]), ([0, 2, 4, 100], [3, 3, 0]), ([0, 2, 4, 7], [3, 3, 0]),
+                         ([2, 3, 6, 6], [2, 4, 1]), ([0, 4, 2, 6], [5, 0, 5]), ([7, 8, 8, 9], [0, 1, 0])):
+        wide = lambda n, fill, dtype=torch.int32: torch.full((n + 16,), fill, dtype=dtype, device="cuda")  # noqa: E731
+        pads = [wide(6, 77), wide(6, 77), wide(6, 77, torch.int64), wide(3, 77), wide(3, 77), wide(12, -1)]
+        slot, pos, mask, seq, held, table = (x[8:-8] for x in pads)
+        held.zero_()
+        free, count = ints(range(12)), ints([12])
+        fa.fa_cache_plan(ints([1, 1, 1]), ints(cu), table.view(3, 4), held, free, count, seq, slot, pos, page_size=8,
+                         max_new=8, parent=ints([-1] * 6), tree_mask=mask.view(6, 1))
+        torch.cuda.synchronize()
+        for x, fill in zip(pads, (77, 77, 77, 77, 77, -1)):
+            assert (x[:8] == fill).all() and (x[-8:] == fill).all(), cu
+        assert seq.tolist() == seq_want, cu
+        pages = [table.view(3, 4)[b, i].item() for b in range(3) for i in range(held[b].item())]
+        assert sorted(pages + free[:count.item()].tolist()) == list(range(12)), cu
+        assert slot.max() < 96 and slot.min() >= -1
+
+
+def test_a_step_of_too_many_rows_leaves_the_request_as_it_was():
+    # Three requests of 8 rows and buffers for 20: the third is refused whole, eagerly and in a replayed graph,
+    # and goes on from where it was in the next step.
+    cache = fa.PagedCache(num_pages=40, page_size=8, batch=3, max_len=100, H_kv=1, d=64, max_rows=20, max_new=8)
+    x = torch.randn((20, 1, 64), device="cuda").to(torch.bfloat16)
+    o, lse = torch.zeros_like(x), torch.zeros((20, 1), device="cuda")
+    new = ints([5, 5, 5])
+
+    def step():
+        cache.plan(new)
+        cache.append(0, x, x, x)
+        cache.attend(0, x, o=o, lse=lse)
+        cache.keep()
+
+    step()
+    assert cache.ctx_len.tolist() == [5, 5, 5]
+    new.copy_(ints([8, 8, 8]))
+    step()
+    torch.cuda.synchronize()
+    assert cache.seq_len.tolist() == [13, 13, 0] and cache.ctx_len.tolist() == [13, 13, 5]
+    assert torch.isfinite(o[:16].float()).all() and torch.isneginf(lse[16:]).all() and (o[16:] == 0).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n, want in (([8, 8, 8], [21, 21, 5]), ([1, 1, 8], [22, 22, 13]), ([8, 0, 13], [30, 22, 13]), ([0, 8, 8], [30, 30, 21])):
+        new.copy_(ints(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert cache.ctx_len.tolist() == want
+    held = sum(cache.n_pages.tolist())
+    assert cache.free_count.item() + held == 40 and held == sum(-(-c // 8) for c in cache.ctx_len.tolist())

@@ -76,6 +76,15 @@ def test_plan_hands_out_each_page_once():
         ctx = [0 if rng.random() < 0.3 else min(int(s), 60) for s in seq]
 
 
+def test_plan_refuses_rows_behind_the_buffers():
+    # 20 rows for 3 x 8 new tokens: the third request keeps its pages and length, its rows get no slot, and one
+    # without new rows behind it is served.
+    args = [[5, 5, 5, 5], [0, 8, 16, 24, 24], [[0, -1], [1, -1], [2, -1], [3, -1]], [1] * 4, [4, 5, 6] + [-1] * 4, 3, 8, 20, 8]
+    table, held, _, count, seq, slot, pos, mask = C.plan(*args, parent=[-1] * 20)
+    assert seq == [13, 13, 0, 5] and held == [2, 2, 1, 1] and count == 1 and table[2] == [2, -1]
+    assert slot[:8] == [5, 6, 7, 48, 49, 50, 51, 52] and slot[16:] == [-1] * 4 and pos[16:] == [5] * 4 and len(mask) == 20
+
+
 def test_commit_moves_a_path():
     rows = np.arange(10)
     assert C.commit(rows, 3, [1, 2, 5]) == 6 and rows.tolist() == [0, 1, 2, 4, 5, 8, 6, 7, 8, 9]
