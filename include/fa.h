@@ -357,7 +357,8 @@ fa_status fa_rope_append(const fa_kv_cache* cache, int rows, int Hq, const fa_ro
  *                    tree_mask [rows][ceil(max_q/64)] is set (a drafted tree).
  * Keys on a page index outside [0, num_pages) are not seen. A row that sees no key
  * gets O = 0, lse = -inf. o [rows][Hq][d]; lse fp32 [rows][Hq], natural log as
- * fa_fwd. Rows of no request stay as they were. What the cache holds behind
+ * fa_fwd. Rows of no request stay as they were. Where cu_q goes beyond `rows`, the
+ * rows there are computed, in their places, and the others are not. What the cache holds behind
  * seq_len[b] is never used, whatever it is; K and V of a request's own keys that some
  * row does not see must be finite in V (P = 0 there multiplies them).
  * block_table int32 [B][max_pages]. Hq a multiple of H_kv; 1 <= B <= 4096; max_q >= 1,

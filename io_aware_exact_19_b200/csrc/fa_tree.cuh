@@ -112,8 +112,8 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
 
 // A run of key tiles of one unit.
 struct Item {
-  int ctx;             // rows of the request before its new ones (seq_len - n; negative: not all are there)
-  int b, q0, n, len;   // request, its first row, its rows, its keys
+  int ctx;             // rows of the request before its new ones (negative: not all are there)
+  int b, q0, n, len;   // request, its first row, its rows (those there), its keys
   int h, r0;           // cache head, first query row (token * G + head in group) of the unit
   int t0, t1;          // key tiles to visit
   int clean;           // tiles before this one are seen whole by every row
@@ -186,7 +186,8 @@ struct Cursor {
       h = rt;
       rt = units - 1 - back;
     }
-    const int r0 = rt * N, ctx = max(p.seq_len[b], 0) - n;
+    // All of the request's rows count for their places, also those behind p.rows.
+    const int r0 = rt * N, ctx = max(p.seq_len[b], 0) - (p.cu_q[b + 1] - q0);
     const int taken = static_cast<int>(min(static_cast<long long>(tiles - t), end - pos));
     int t1 = (len + kKeys - 1) / kKeys;
     if (!p.by_unit) t1 = min(t + taken, t1);
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(128 * (N > 32 ? N / 32 : 1) + 96, 1)
         if (t >= clean) {
         const bool alive = key < len;
         seen = alive ? ~0u : 0u;
-        const long long own = key - it.ctx;  // its index among the new tokens
+        const long long own = static_cast<long long>(key) - it.ctx;  // its index among the new tokens
         const int first_row = it.r0 + col0;
         if (p.tree_mask == nullptr) {
           if (alive && own >= 0) {

@@ -4,8 +4,9 @@ import pytest
 import torch
 
 import io_aware_exact_19_b200 as fa
-from tests.cache_cases import ints, random_parents
+from tests.cache_cases import Paged, assert_attention, attention_reference, f64, ints, random_parents
 from tests.test_cache_gpu import State
+from tests.test_tree_gpu import attend, mask_of, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,21 @@ def test_a_step_of_too_many_rows_leaves_the_request_as_it_was():
         assert cache.ctx_len.tolist() == want
     held = sum(cache.n_pages.tolist())
     assert cache.free_count.item() + held == 40 and held == sum(-(-c // 8) for c in cache.ctx_len.tolist())
+
+
+@pytest.mark.parametrize("ctx,new,rows,Hq,H_kv,d,tree", [
+    ([40, 300], [6, 9], 11, 4, 2, 64, False), ([40, 300], [6, 9], 11, 4, 2, 64, True),
+    ([200, 90], [3, 60], 40, 8, 2, 128, False), ([200, 90], [3, 60], 40, 8, 2, 128, True),
+    ([50, 130], [7, 30], 12, 2, 1, 256, False), ([500, 300, 700], [200, 333, 300], 700, 32, 8, 64, False),
+])
+def test_rows_behind_the_batch_leave_the_others_in_their_places(ctx, new, rows, Hq, H_kv, d, tree):
+    # cu_q goes beyond the rows that are given: those there are the first of their request, not the last.
+    p = Paged(ctx, new, H_kv, d, 16, "bf16", seed=rows)
+    bits, mask = mask_of(p, random_parents(new, p.rng)) if tree else (None, None)
+    q = queries(p, Hq)
+    ref = attention_reference(p, f64(q), d ** -0.5, bits)
+    o, lse = attend(p, q[:rows], None if mask is None else mask[:rows].contiguous())
+    there = [max(0, min(n, rows - int(t0))) for n, t0 in zip(new, p.cu_host)]
+    p.new = there
+    assert sum(there) == rows
+    assert_attention(p, o, lse, [(O[:m], L[:m], size[:m], big) for m, (O, L, size, big) in zip(there, ref)])
