@@ -105,8 +105,8 @@ __device__ __forceinline__ void plan_pages(const PlanArgs& p, int* smem) {
       const int held = min(max(p.n_pages[b], 0), p.max_pages);
       const long long pages = (static_cast<long long>(ctx) + n + (1 << p.page_shift) - 1) >> p.page_shift;
       // New rows behind the buffers get no slot and so are never written: none of the request's are then.
-      const bool inside = n == 0 || (cu >= 0 && cu + n <= p.rows);
-      const bool ok = ctx >= 0 && n >= 0 && n <= p.max_new && inside && pages <= p.max_pages;
+      const bool inside = (n == 0) | ((cu >= 0) & (cu + n <= p.rows));
+      const bool ok = (ctx >= 0) & (n >= 0) & (n <= p.max_new) & inside & (pages <= p.max_pages);
       const int want = ok ? static_cast<int>(pages) : -1;
       s_cu[b] = cu;
       s_ctx[b] = ctx;
