@@ -105,11 +105,12 @@ class PagedCache:
 
     def append(self, layer: int, q, k, v, rope: Rope | None = None, q_out=None):
         """Write the step's rows ``k`` and ``v`` [T, H_kv, d] to their slots; returns ``q`` rotated (and
-        rotates ``k``) by ``rope``. Rows past the step's last (a padded batch) are not written."""
+        rotates ``k``) by ``rope``, in ``q_out`` if it is given. Without ``rope`` nothing is rotated: ``q`` is
+        returned, or copied into ``q_out``. Rows past the step's last (a padded batch) are not written."""
         T = k.shape[0]
         if rope is None:
-            paged.fa_rope_append(None, k, v, None, self.k[layer], self.v[layer], self.slot[:T])
-            return q
+            paged.fa_rope_append(None if q_out is None else q, k, v, q_out, self.k[layer], self.v[layer], self.slot[:T])
+            return q if q_out is None else q_out
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
         positions = rope.positions
         if positions is None:  # the plan's, on as many axes as the tables may name

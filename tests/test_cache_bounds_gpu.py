@@ -93,3 +93,16 @@ def test_rows_behind_the_batch_leave_the_others_in_their_places(ctx, new, rows, 
     p.new = there
     assert sum(there) == rows
     assert_attention(p, o, lse, [(O[:m], L[:m], size[:m], big) for m, (O, L, size, big) in zip(there, ref)])
+
+
+def test_append_without_a_rotation_fills_the_buffer():
+    # A step with fixed buffers reads its queries there, rotated or not.
+    cache = fa.PagedCache(num_pages=4, page_size=16, batch=1, max_len=64, H_kv=1, d=64, max_rows=6, max_new=6)
+    packed = torch.randn((6, 6, 64), device="cuda").to(torch.bfloat16)
+    q, k, v = packed.split([4, 1, 1], 1)
+    q_out = torch.full((6, 4, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    cache.plan(ints([6]))
+    assert cache.append(0, q, k, v, q_out=q_out) is q_out and torch.equal(q_out, q)
+    first = cache.block_table[0, 0].item()
+    assert torch.equal(cache.k[0, first, 0, :6], k[:, 0]) and torch.equal(cache.v[0, first, 0, :6], v[:, 0])
+    assert cache.append(0, q, k, v) is q
