@@ -55,9 +55,11 @@ class Rope:
     def turn(self, x, out=None, inverse: bool = False, stream=None):
         """``x`` [B, H, N, d] rotated (into a new tensor unless ``out`` is given)."""
         if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            # Memory of the stream that writes it: the current stream's could still be in use there.
+            with torch.cuda.stream(stream):
+                out = torch.empty_like(x, memory_format=torch.contiguous_format)
             if stream is not None:
-                out.record_stream(stream)
+                out.record_stream(torch.cuda.current_stream(x.device))
         paged.fa_rope(x, out, self.positions, self.inv_freq, self.axis, inverse=inverse, pairs=self.pairs, stream=stream)
         return out
 

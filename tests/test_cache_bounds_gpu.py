@@ -1,4 +1,5 @@
-"""Steps whose rows do not fit the buffers they are given, and PagedCache's optional buffers."""
+"""Steps whose rows do not fit the buffers they are given, PagedCache's optional buffers, rotations on
+another stream."""
 import numpy as np
 import pytest
 import torch
@@ -106,3 +107,46 @@ def test_append_without_a_rotation_fills_the_buffer():
     first = cache.block_table[0, 0].item()
     assert torch.equal(cache.k[0, first, 0, :6], k[:, 0]) and torch.equal(cache.v[0, first, 0, :6], v[:, 0])
     assert cache.append(0, q, k, v) is q
+
+
+def test_rotation_on_another_stream_takes_no_memory_still_in_use():
+    # A freed block of the current stream is still to be written there; the rotated tensor, written on another
+    # stream at once, must not lie in it, and must not be handed out again before its own work is done.
+    rope = fa.Rope(*fa.rope_tables(64), positions=torch.arange(512, dtype=torch.int32, device="cuda")[None])
+    x = torch.randn((2, 4, 512, 64), device="cuda").to(torch.bfloat16)
+    side = torch.cuda.Stream()
+    want, minus, after = rope.turn(x), -x, torch.empty_like(x)
+    rope.turn(x, after)
+    torch.cuda.synchronize()
+    old = torch.empty_like(x)
+    where = old.data_ptr()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    old.fill_(7.0)
+    del old
+    out = rope.turn(x, stream=side)
+    assert out.data_ptr() != where
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    # used on the current stream and let go: the block waits for that use
+    side.synchronize()
+    torch.cuda._sleep(100_000_000)
+    after.copy_(out)
+    del out
+    again = rope.turn(minus, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(after, want) and torch.equal(again, -want)
+
+
+def test_attention_with_rotation_on_another_stream():
+    rope = fa.Rope(*fa.rope_tables(64), positions=torch.arange(300, dtype=torch.int32, device="cuda")[None])
+    q, k, v, do = (torch.randn((1, 2, 300, 64), device="cuda").to(torch.bfloat16) for _ in range(4))
+    o, lse = fa.attention_forward(q, k, v, causal=True, rope=rope)
+    want = (o, lse, *fa.attention_backward(q, k, v, o, lse, do, causal=True, rope=rope))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o, lse = fa.attention_forward(q, k, v, causal=True, rope=rope, stream=side)
+    workspace = torch.empty(fa.fa_bwd_workspace_size(1, 2, 300, 64), dtype=torch.uint8, device="cuda")
+    got = (o, lse, *fa.attention_backward(q, k, v, o, lse, do, causal=True, rope=rope, workspace=workspace, stream=side))
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
