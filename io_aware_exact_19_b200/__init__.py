@@ -422,7 +422,8 @@ def attention_backward(q, k, v, o, lse, dout, causal: bool = False, block_mask=N
         q, k = rope.turn(q, stream=stream), rope.turn(k, stream=stream)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), dtype=torch.uint8, device=q.device)
+        with torch.cuda.stream(stream):  # let go at the end of this call: memory of the stream that uses it
+            workspace = torch.empty(fa_bwd_workspace_size(B, H, N, d), dtype=torch.uint8, device=q.device)
     if block_mask is None:
         fa_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, causal, scale, stream)
     else:

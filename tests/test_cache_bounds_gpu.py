@@ -150,3 +150,17 @@ def test_attention_with_rotation_on_another_stream():
     side.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_backward_on_another_stream_keeps_its_workspace_to_itself(monkeypatch):
+    # The workspace that the call makes is let go at its end, with its kernels still to run (here: none is
+    # launched): the current stream must not get that memory.
+    q, k, v, do, o = (torch.zeros((1, 2, 256, 64), dtype=torch.bfloat16, device="cuda") for _ in range(5))
+    lse, side, seen = torch.zeros((1, 2, 256), device="cuda"), torch.cuda.Stream(), []
+    monkeypatch.setattr(fa, "fa_bwd", lambda *a: seen.append((a[9].data_ptr(), a[9].numel())))
+    fa.attention_backward(q, k, v, o, lse, do, stream=side)
+    (at, size), = seen
+    assert size == fa.fa_bwd_workspace_size(1, 2, 256, 64)
+    assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != at
+    with torch.cuda.stream(side):
+        assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() == at
