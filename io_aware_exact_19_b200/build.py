@@ -73,19 +73,31 @@ def _check_launch_registers(src: str) -> None:
                 raise RuntimeError(f"{mangled}: {regs} registers at launch, the register split needs {want}")
 
 
+def binding_stamp() -> str:
+    """What _paged.so is compiled against: it reads tensors through torch's inline accessors, so it
+    serves this interpreter and this torch alone."""
+    import sysconfig
+
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')} torch-{torch.__version__} cxx11-{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
 def _build_binding() -> None:
     """Compile the paged cache's Python binding (_paged.so, against this interpreter and torch)."""
     import sysconfig
 
     import torch
     src, root = os.path.join(CSRC, "paged_binding.cpp"), os.path.dirname(torch.__file__)
+    stamp, stamp_at = binding_stamp(), os.path.join(BUILD, "paged_binding.stamp")
     newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "fa.h"), __file__))
-    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return
-    tmp = BINDING + ".tmp"
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest and os.path.exists(stamp_at):
+        with open(stamp_at) as f:
+            if f.read() == stamp:
+                return
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-o", tmp, src,
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DFA_BUILT_FOR="{stamp}"',
            *(x for d in (sysconfig.get_paths()["include"], INCLUDE, os.path.join(root, "include"),
                          os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"))
              for x in ("-isystem", d)),
@@ -94,6 +106,8 @@ def _build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"the compiler failed for paged_binding.cpp:\n{r.stderr[-4000:]}")
     os.replace(tmp, BINDING)
+    with open(stamp_at, "w") as f:
+        f.write(stamp)
 
 
 def build(verbose: bool = False) -> str:

@@ -345,4 +345,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__paged() {
+  PyObject* m = PyModule_Create(&module);
+  // The interpreter and torch that it was compiled against (the build passes them in).
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", FA_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

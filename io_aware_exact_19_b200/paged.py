@@ -12,6 +12,7 @@ import ctypes
 import torch  # noqa: F401  (its libraries are loaded before the binding's)
 
 from . import FAError, load_library
+from .build import binding_stamp
 
 TREE_MAX = 512  # FA_TREE_MAX: tokens of a drafted tree
 
@@ -30,11 +31,14 @@ class RowsDesc(ctypes.Structure):
 
 
 def _load_binding():
+    missing = ("the binding _paged.so is missing or was built for another torch; run "
+               "`python -m io_aware_exact_19_b200.build`")
     try:
         from . import _paged
     except ImportError as e:
-        raise FileNotFoundError("the binding _paged.so is missing or was built for another torch; run "
-                                "`python -m io_aware_exact_19_b200.build`") from e
+        raise FileNotFoundError(missing) from e
+    if getattr(_paged, "built_for", None) != binding_stamp():
+        raise FileNotFoundError(missing)
     lib = load_library()
     _paged.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
                   ("fa_cache_plan", "fa_rope", "fa_rope_append", "fa_tree_fwd", "fa_tree_fwd_workspace_size",
