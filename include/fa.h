@@ -302,9 +302,10 @@ typedef struct {
  * [num_pages], of which the first *free_count are free; ctx_len, seq_len [B]; cu_new
  * [B+1]; slot, position, parent [rows], all int32 on the DEVICE. block_table,
  * n_pages, free_list and free_count are the cache's state and updated in place:
- * calls on one cache must be ordered. parent and tree_mask are both given or both
- * NULL. 1 <= B <= 4096, 0 <= rows, 1 <= max_new (with parent: <= 512, else
- * FA_ERR_UNSUPPORTED). One launch.
+ * calls on one cache must be ordered. cu_new must not fall: the requests before and
+ * behind a negative n_b would claim the same rows, of which each gets one slot. parent
+ * and tree_mask are both given or both NULL. 1 <= B <= 4096, 0 <= rows, 1 <= max_new
+ * (with parent: <= 512, else FA_ERR_UNSUPPORTED). One launch.
  */
 #define FA_TREE_MAX 512
 fa_status fa_cache_plan(int B, int rows, int max_new, int page_size, int num_pages, int max_pages,
@@ -323,10 +324,11 @@ fa_status fa_cache_plan(int B, int rows, int max_new, int page_size, int num_pag
  * gradient. Angles are reduced in 64 bits, so far positions lose nothing.
  * x, out [B, H, N, d] with element strides of b, h and n (multiples of 8; the d
  * elements contiguous; 16-byte aligned; those of out at least d where there is more
- * than one); out may be x itself, but must not overlap it in another way. positions int32 [n_axes][B][N] with element strides of axis and
- * b (0: shared by the batch); inv_freq fp32 [rot/2]; axis uint8 [rot/2], an entry
- * >= n_axes leaves its pair unturned. rot a multiple of 16, 16..d; 1 <= n_axes <= 8;
- * d as for the forward entry points.
+ * than one); out may be x itself, but must not overlap it in another way. positions
+ * int32 [n_axes][B][N] with element strides of axis and b (0: shared by the batch);
+ * inv_freq fp32 [rot/2]; axis uint8 [rot/2], an entry >= n_axes leaves its pair
+ * unturned. rot a multiple of 16, 16..d; 1 <= n_axes <= 8; d as for the forward entry
+ * points.
  */
 fa_status fa_rope(fa_dtype dtype, const void* x, void* out, int B, int H, int N, int d, const long long x_strides[3],
                   const long long out_strides[3], const int32_t* positions, long long pos_axis_stride,
@@ -337,8 +339,8 @@ fa_status fa_rope(fa_dtype dtype, const void* x, void* out, int B, int H, int N,
  * The same rotation of a step's new q and k, with k and v written to the cache:
  * q -> q_out [rows][Hq][d], k and v [rows][H_kv][d] -> row slot[t] of the cache (page
  * slot / page_size, row slot % page_size). A slot outside the cache (-1) writes
- * nothing; two rows with one slot leave either. positions int32 [n_axes][rows] with
- * an axis stride. q and q_out may both be NULL (k and v only) and q_out may be q.
+ * nothing; two rows with one slot leave pieces of both. positions int32 [n_axes][rows]
+ * with an axis stride. q and q_out may both be NULL (k and v only) and q_out may be q.
  * rot = 0 rotates nothing (positions, inv_freq, axis are not read). One launch.
  */
 fa_status fa_rope_append(const fa_kv_cache* cache, int rows, int Hq, const fa_rows* q, const fa_rows* k,
@@ -381,8 +383,8 @@ fa_status fa_tree_fwd(const fa_kv_cache* cache, const fa_rows* q, const fa_rows*
  * n_accepted has to be 0, since nothing was written). accepted int32 [B][max_accept]
  * holds request-local indices of new tokens, strictly increasing (a path from the root
  * is); the path ends before the first entry that is not larger than the one before (or
- * is negative), or whose row has no page in the table. new_len may be ctx_len. DEVICE pointers; ctx_len,
- * n_accepted, new_len int32 [B]. One launch.
+ * is negative), or whose row has no page in the table. new_len may be ctx_len. DEVICE
+ * pointers; ctx_len, n_accepted, new_len int32 [B]. One launch.
  */
 fa_status fa_cache_commit(const fa_kv_cache* cache, int B, int max_pages, int max_accept, const int32_t* block_table,
                           const int32_t* ctx_len, const int32_t* accepted, const int32_t* n_accepted,

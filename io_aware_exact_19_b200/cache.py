@@ -7,7 +7,9 @@ them in the order of a serving step:
     for each layer:
         q = cache.append(layer, q, k, v, rope)      rotate, write K and V   (one launch)
         o = cache.attend(layer, q)                  attention               (one or two)
-    cache.commit(accepted, count)  or  cache.keep() the rows that stay
+    cache.commit(accepted, count)  or  cache.keep() the rows that stay      (one a layer; none)
+
+Beside these launches plan, commit and keep run two or three, two and one small operations of torch.
 
 Everything runs on the current stream. Lengths, tables and maps stay on the GPU, so a step can
 be captured in a CUDA graph (after one run outside it) and replayed with other lengths in the
@@ -91,7 +93,8 @@ class PagedCache:
         GPU, at most ``most`` each; the attention is quickest when that is close): their slots and
         positions, and with ``parent`` (int32, one for each new row) the masks of drafted trees.
         ``seq_len[b]`` is 0 where the pages did not suffice, and where a request's rows go beyond the
-        step's ``max_rows``."""
+        step's ``max_rows``. Pages are granted in the order of the requests, and one that gets none holds up
+        those behind it that need some: leave it out of the step (``new[b] = 0``) until pages are back."""
         self.most = self.max_new if most is None else most
         if not 1 <= self.most <= self.max_new:
             raise ValueError(f"most must lie in 1..{self.max_new}")

@@ -13,12 +13,13 @@ namespace {
 // ------------------------------------------------------------------ plan
 //
 // Latency bound: the floor is a launch and the loads that wait for one another (lengths, free
-// pages, table). Measured: 4.3 us for 8 requests' next tokens, 6.4 for 256 trees of up to 64 tokens
-// (16.5 with pages by a warp per request and the trees behind them in the same CTAs). The pages are handed out by one cluster of 8 CTAs, so that the two places where
-// all requests meet (pages given back before any is taken, tables written before slots are read)
-// are cluster barriers and the whole plan is one launch. Every CTA reads all lengths and scans
-// the needs itself, one load's latency, which is cheaper than handing prefix sums around; pages
-// are then given out a thread per page and slots a thread per row.
+// pages, table). Measured, back to back and with every page already held: 4.3 us for 8 requests' next
+// tokens, 6.4 for 256 trees of up to 64 tokens (16.5 with pages by a warp per request and the trees
+// behind them in the same CTAs). The pages are handed out by one cluster of 8 CTAs, so that the two
+// places where all requests meet (pages given back, if there are any, before any is taken; tables
+// written before slots are read) are cluster barriers and the whole plan is one launch. Every CTA reads
+// all lengths and scans the needs itself, one load's latency, which is cheaper than handing prefix sums
+// around; pages are then given out a thread per page and slots a thread per row.
 //
 // Tree masks need no pages: further clusters build them at the same time. The set of a token's
 // ancestors by pointer doubling: with A_t the mask known so far and up_t the first token not in

@@ -19,10 +19,14 @@ int row_tile(int max_q, int group, int D) {
 
 int padded_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
 
-// Prompt chunks with at least a unit for every SM are not cut: whole units, the longest first. (H_kv =
-// 8, groups of 4, d = 128: one prompt of 1024 rows 44 us cut and 27 not, 2048 rows 90 and 62, 8192
-// rows 970 and 566; 8 x 128 rows over 3000 keys 78 and 71; 4 x 300 rows over 1000 keys 50 and 51. Fewer
-// or smaller units are cut: they go with long caches, whose lengths would not even out.)
+// Prompt chunks with at least a unit for every SM are not cut. (H_kv = 8, groups of 4, d = 128: one
+// prompt of 1024 rows 44 us cut and 27 not, 2048 rows 90 and 62, 8192 rows 970 and 566; 8 x 128 rows over
+// 3000 keys 78 and 71; 40 of 300 rows behind 0 to 30000 keys 4700 and 3500; 64 single rows over 1000 to
+// 8000 keys next to a prompt of 1024 230 and 210.) The rule counts units, since only the device knows their
+// lengths, and loses where few units are long: where the last wave of them is nearly empty (just above
+// 148 units: 600 rows behind 20000 keys at d = 64 188 us cut and 335 not, 330 x 7 behind 25000 245 and 437,
+// 2 x 300 behind 3000 57 and 69; 312 units behind 20000 445 and 550), and where a long request stands next
+// to a prompt (one row over 64K keys, 1024 rows over none: 89 and 549).
 bool by_unit(int rows, int max_q, int Hq, int H_kv, int tile) {
   const long long units = static_cast<long long>(H_kv) * ((static_cast<long long>(rows) * (Hq / H_kv) + tile - 1) / tile);
   return static_cast<long long>(max_q) * (Hq / H_kv) >= 512 && units >= tree::kMaxWorkers;

@@ -23,7 +23,8 @@
 // (O, log2-sum-exp) pairs which fa_tree_merge_kernel joins (the update of the interview
 // explainer, section 3.2, applied to runs of keys), in the order of the keys, so the
 // result does not depend on which CTA ends first. Prompt chunks, whose units are many and
-// long, are not cut: each CTA takes whole units, the longest first.
+// long, are not cut: each CTA takes whole units, request by request as they stand in the batch,
+// and of a request the last row tiles, which see the most keys, first (see by_unit in fa_tree.cu).
 //
 // Warp roles: a softmax warpgroup for every 32 columns (a thread holds its key's scores for
 // them), then a TMA producer warp for K, the MMA warp, and a producer warp for V.
